@@ -9,8 +9,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqi.so")
-SOURCES = ["qi_api.cu", "qi_gemm.cu", "qi_quant.cu", "qi_misc.cu", "qi_attn_tc.cu"]
-HEADERS = ["qi_common.cuh", "qi_internal.h"]
+SOURCES = ["qi_api.cu", "qi_gemm.cu", "qi_quant.cu", "qi_misc.cu", "qi_attn_tc.cu",
+           "qi_layer_api.cu", "qi_linear.cu", "qi_attn_packed.cu"]
+HEADERS = ["qi_common.cuh", "qi_tc.cuh", "qi_mx.cuh", "qi_internal.h", "qi_host.h"]
 
 
 def nvcc() -> str:
@@ -38,16 +39,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
              "--expt-relaxed-constexpr"]
     if verbose:
         flags += ["-Xptxas", "-v"]
-    objs = []
-    for src in SOURCES:
-        obj = os.path.join(build_dir, src.replace(".cu", ".o"))
-        cmd = [nvcc(), *flags, "-cudart", "static", "-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0 or verbose:
-            sys.stderr.write(r.stdout + r.stderr)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}")
-        objs.append(obj)
+    objs = [os.path.join(build_dir, src.replace(".cu", ".o")) for src in SOURCES]
+    runs = [subprocess.Popen([nvcc(), *flags, "-cudart", "static", "-c", os.path.join(CSRC, src),
+                              "-o", obj], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+            for src, obj in zip(SOURCES, objs)]
+    failed = []
+    for src, run in zip(SOURCES, runs):
+        log = run.communicate()[0]
+        if run.returncode != 0 or verbose:
+            sys.stderr.write(log)
+        if run.returncode != 0:
+            failed.append(src)
+    if failed:
+        raise RuntimeError(f"nvcc failed on {', '.join(failed)}")
     tmp = LIB + ".tmp"
     cmd = [nvcc(), "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-cudart", "static",
            *objs, "-o", tmp]

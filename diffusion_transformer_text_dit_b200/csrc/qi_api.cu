@@ -10,79 +10,12 @@
 
 #include <algorithm>
 #include <mutex>
-#include <string>
 
-#include "qi.h"
-#include "qi_common.cuh"
-#include "qi_internal.h"
+#include "qi_host.h"
 
-// Optional per-launch timing: when enabled, every kernel launch of the library
-// is bracketed by a pair of CUDA events on its stream; durations are summed per
-// kernel class when read back.  Launches are counted per class either way.
-constexpr int QI_PROF_CLASSES = 8;
-constexpr int QI_PROF_MAX_PAIRS = 16384;
-
-struct qi_ctx {
-  int device;
-  int num_sms;
-  int* status;   // device status word
-  bool prof_on;
-  int prof_used;
-  cudaEvent_t* prof_ev;          // [2 * QI_PROF_MAX_PAIRS]
-  int* prof_cls;                 // [QI_PROF_MAX_PAIRS]
-  long long launches[QI_PROF_CLASSES];
-  int attn_fp8;                  // steps run e4m3 attention (qi_ctx_set_attention_fp8)
-  bool taps_on;                  // copy the quantizers' inputs and outputs (qi_ctx_set_block_taps)
-  qi_block_taps taps;
-  void* attn_scratch;            // key-range split scratch of qi_attn_block_causal(_fp8)
-  size_t attn_scratch_bytes;
-};
+using namespace qi_host;
 
 namespace {
-
-thread_local std::string g_last_error;
-
-int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-int fail(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return code;
-}
-
-int cuda_fail(const char* what) {
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) {   // already read by the launcher
-    e = qi::last_launch_error();
-    qi::last_launch_error() = cudaSuccess;
-  }
-  return fail(QI_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-cudaStream_t S(void* s) { return static_cast<cudaStream_t>(s); }
-
-struct Prof {
-  qi_ctx* c;
-  int slot;
-  cudaStream_t st;
-  Prof(qi_ctx* ctx, int cls, cudaStream_t s) : c(ctx), slot(-1), st(s) {
-    if (!c) return;
-    c->launches[cls] += 1;
-    if (c->prof_on && c->prof_used < QI_PROF_MAX_PAIRS) {
-      slot = c->prof_used++;
-      c->prof_cls[slot] = cls;
-      cudaEventRecord(c->prof_ev[2 * slot], st);
-    }
-  }
-  ~Prof() {
-    if (slot >= 0) cudaEventRecord(c->prof_ev[2 * slot + 1], st);
-  }
-};
 
 // Validate a group table against a sequence length; fill the device-side copy.
 int check_groups(const qi_groups* g, int total, qi::GroupTable* out) {
@@ -154,19 +87,6 @@ int check_bf16_linear(const qi_linear_bf16* w, const char* name, int n, int k) {
     return fail(QI_ERR_ALIGNMENT, "BF16 weight %s: pointers must be 16-byte aligned", name);
   return QI_OK;
 }
-
-// Bump allocator over the caller's workspace (256-byte aligned pieces).
-struct Carve {
-  uint8_t* base;
-  size_t cap, off;
-  template <class T>
-  T* take(size_t count) {
-    off = (off + 255) & ~static_cast<size_t>(255);
-    T* p = reinterpret_cast<T*>(base ? base + off : nullptr);
-    off += count * sizeof(T);
-    return p;
-  }
-};
 
 struct BlockBufs {
   int8_t* uq;       // [T, max(H, F)]
@@ -246,9 +166,7 @@ StepBufs carve_step(Carve& c, const qi_dims& d, int Sq, int S, bool own_kv) {
 
 namespace qi {
 
-bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, uint64_t inner,
-                  uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
-                  uint32_t box_outer, bool swizzle128) {
+static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (!encode) {
     void* fn = nullptr;
@@ -256,9 +174,17 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, ui
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) !=
             cudaSuccess ||
         q != cudaDriverEntryPointSuccess || !fn)
-      return false;
+      return nullptr;
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
+  return encode;
+}
+
+bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, uint64_t inner,
+                  uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
+                  uint32_t box_outer, bool swizzle128) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
+  if (!encode) return false;
   cuuint64_t dims[2] = {inner, outer};
   cuuint64_t strides[1] = {row_stride_bytes};
   cuuint32_t box[2] = {box_inner, box_outer};
@@ -269,6 +195,20 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, ui
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_rows3(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t rows,
+                     uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_mid,
+                     uint32_t box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
+  if (!encode) return false;
+  cuuint64_t dims[3] = {inner, mid, rows};
+  cuuint64_t strides[2] = {inner * 2, row_stride_bytes};
+  cuuint32_t box[3] = {box_inner, box_mid, box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace qi

@@ -19,6 +19,7 @@
 // columns) so the epilogue of tile i overlaps the MMAs of tile i+1.
 #include "qi_common.cuh"
 #include "qi_mx.cuh"
+#include "qi_tc.cuh"
 #include "qi_internal.h"
 
 namespace qi {
@@ -39,19 +40,6 @@ struct GemmCfg {
   static constexpr int SMEM_BYTES = 1024 /*align slack*/ + STAGES * STAGE_BYTES + 256 + COL_BYTES;
   static_assert(2 * STAGES + 8 <= 32, "barrier area");
 };
-
-// GELU, tanh form: 0.5 x (1 + tanh(z)), z = sqrt(2/pi) (x + 0.044715 x^3).
-// Evaluated as x / (1 + e^(-2z)) (the same function: 0.5 (1 + tanh z) is the
-// logistic of 2z), with the hardware base-2 exponential and a fast divide;
-// relative error ~1e-6, far below the bf16 rounding of the result.
-__device__ __forceinline__ float gelu_tanh_f(float x) {
-  const float k0 = 0.7978845608028654f;   // sqrt(2/pi)
-  const float k1 = 0.044715f;
-  const float z = k0 * fmaf(k1 * x, x * x, x);
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-2.8853900817779268f * z));   // e^(-2z)
-  return __fdividef(x, 1.0f + e);
-}
 
 // Per-column constants of one tile (s_w, rowsum, bias as fp32), staged in
 // shared memory by the epilogue warps so that each output element reads them
@@ -419,24 +407,6 @@ __device__ __forceinline__ void epilogue_tile(const GemmParams& p, const ColTabl
   }
 }
 
-// Tile order of the persistent loops.  Tiles are walked in groups of
-// group_m consecutive M tiles: inside a group M varies fastest, then N; the
-// groups follow each other along M.  The tiles in flight at one time then
-// share a band of A rows and a band of B columns.  group_m = m_tiles is the
-// plain M-fastest order, in which every wave of tiles re-reads all of A: right
-// when A is small enough to stay in L2, wasteful when it is not (the MLP down
-// projection's A is 75 MB at 4608 x 16384).
-__device__ __forceinline__ void tile_coords(int tile, int m_tiles, int group_m, int n_tiles,
-                                            int& mt, int& nt) {
-  const int per_group = group_m * n_tiles;
-  const int g = tile / per_group;
-  const int first = g * group_m;
-  const int gm = min(group_m, m_tiles - first);
-  const int local = tile - g * per_group;
-  mt = first + local % gm;
-  nt = local / gm;
-}
-
 template <bool I8, int BN, int EPI>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -630,109 +600,6 @@ static_assert(3 * PAIR_STAGES + 8 <= 32, "barrier area");
 constexpr int MX_CODE_BYTES = 128 * 32;
 constexpr int PAIR_SMEM_BYTES_MX = PAIR_SMEM_BYTES + PAIR_STAGES * MX_CODE_BYTES;
 static_assert(PAIR_SMEM_BYTES_MX <= 232448, "shared memory per CTA");
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-
-// Address of the same shared-memory object in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-
-// Every thread of both CTAs; orders shared-memory and barrier set-up (release /
-// acquire at cluster scope).  The non-.aligned form: lanes may arrive apart.
-__device__ __forceinline__ void cluster_sync_all() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-  __syncwarp();
-}
-
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// Bounded wait for a phase completed by arrivals from both CTAs of the pair.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, int* status) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait_cluster(bar, parity)) return true;
-    if (has_error(status)) return false;
-    if (globaltimer_ns() - t0 > QI_WAIT_NS) {
-      set_error(status, QI_DEV_ERR_TIMEOUT);
-      return false;
-    }
-  }
-}
-
-// TMA tile load into this CTA's shared memory whose completion is counted on
-// an mbarrier of either CTA of the pair (`bar_cluster` is a shared::cluster
-// address).  Plain load: no multicast.
-__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_t bar_cluster,
-                                                 void* smem, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y)
-      : "memory");
-}
-
-__device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t a, uint64_t b,
-                                             uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
-}
-
-__device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t a, uint64_t b,
-                                              uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
-}
-
-// Arrive on the barrier at this offset in every CTA of `mask` once all MMAs
-// issued so far by this thread have completed.
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(mask)
-      : "memory");
-}
-
-// TMEM allocation / release for a CTA pair: one warp of each CTA executes it;
-// the same columns are allocated in both SMs.
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                   smem_u32(dst)),
-               "r"(ncols));
-}
-__device__ __forceinline__ void tmem_relinquish_pair() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-}
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols));
-}
 
 // ---------------------------------------------------------------- MXFP4 B operand
 //

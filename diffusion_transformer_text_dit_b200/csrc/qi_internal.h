@@ -127,6 +127,12 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, ui
                   uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
                   uint32_t box_outer, bool swizzle128 = true);
 
+// TMA descriptor for bf16 rows [rows][mid][inner] (mid contiguous pieces of
+// `inner` values per row), box box_inner x box_mid x box_rows, 128-byte swizzle.
+bool make_tmap_rows3(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t rows,
+                     uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_mid,
+                     uint32_t box_rows);
+
 int pick_block_n(int N);
 int launch_gemm(bool int8, int epi, const void* A, int lda, const void* B, int ldb,
                 const GemmParams& p, int num_sms, cudaStream_t st);
@@ -264,5 +270,99 @@ int launch_bf16_to_e4m3(const uint16_t* x, uint8_t* y, int64_t n, cudaStream_t s
 // one rounding per operation; v_out (optional) receives v.
 int launch_cfg_euler(float* x, const float* v_c, const float* v_u, int64_t n, float g, float dt,
                      float* v_out, cudaStream_t st);
+
+// ---------------------------------------------------------------- prompt-encoder layer
+
+// Activation applied to a Linear's fp32 value (qi_act values).
+enum MmAct { ACT_NONE = 0, ACT_GELU_TANH = 1, ACT_SILU = 2 };
+
+// BF16 Linear with bias, activation and residual (qi_linear_act):
+//   y = bf16(act(a w^T + bias) + res)
+struct LinearActParams {
+  const uint16_t* a;      // [M, lda]
+  int M, K, N, lda;
+  const uint16_t* w;      // [N, K]
+  const uint16_t* bias;   // [N] or null
+  int act;
+  const uint16_t* res;    // [M, ld_res] or null
+  int ld_res;
+  uint16_t* y;            // [M, ldy]
+  int ldy;
+  int num_sms;
+  int* status;
+};
+int launch_linear_act(const LinearActParams& p, cudaStream_t st);
+
+// Gate and up projections with the activation and the product in one kernel:
+//   h = bf16(act(x gate^T) * (x up^T)), optionally gu = bf16(x gate^T | x up^T)
+struct GateUpParams {
+  const uint16_t* x;      // [M, ldx]
+  int M, H, F, ldx;
+  const uint16_t* gate;   // [F, H]
+  const uint16_t* up;     // [F, H]
+  int act;
+  uint16_t* h;            // [M, F]
+  uint16_t* gu;           // [M, 2F] or null
+  int num_sms;
+  int* status;
+};
+int launch_gate_up(const GateUpParams& p, cudaStream_t st);
+
+// Gradients of the gated feed-forward block; see qi_gated_ffn_backward.
+struct GatedBackwardParams {
+  const uint16_t* x;      // [M, ldx]
+  const uint16_t* dy;     // [M, ld_dy]
+  const uint16_t* gu;     // [M, 2F] saved gate | up
+  int M, H, F, ldx, ld_dy;
+  const uint16_t* gate;
+  const uint16_t* up;
+  const uint16_t* down;   // [H, F]
+  int act;
+  uint16_t* dg;           // [M, F] scratch
+  uint16_t* du;           // [M, F] scratch
+  uint16_t* h;            // [M, F] scratch
+  uint16_t* dx;           // [M, ld_dx] or null
+  int ld_dx;
+  uint16_t* dgate;        // [F, H] or null
+  uint16_t* dup;          // [F, H] or null
+  uint16_t* ddown;        // [H, F] or null
+  int num_sms;
+  int* status;
+};
+int launch_gated_dh(const GatedBackwardParams& p, cudaStream_t st);        // dg, du, h
+int launch_gated_dx(const GatedBackwardParams& p, cudaStream_t st);        // dx
+int launch_gated_dw(const GatedBackwardParams& p, cudaStream_t st);        // the weights' gradients
+
+// Causal attention over packed sequences with grouped heads (qi_attn_causal_packed).
+constexpr int AP_MAX_SEQS = 256;
+struct PackedPlan {
+  int n_seqs;             // sequences with queries
+  int G, P;               // query heads per key/value head; query positions per 128-row tile
+  int nq;                 // 128-row query tiles per CTA (1 or 2)
+  int units;              // CTAs
+  int slots;              // partial results (0: no sequence is split over its keys)
+  int slot_rows;          // rows of one partial result
+  int groups;             // CTAs of the combining kernel
+  // sequences in launch order
+  int q0[AP_MAX_SEQS], ql[AP_MAX_SEQS], k0[AP_MAX_SEQS], kl[AP_MAX_SEQS];
+  int nsp[AP_MAX_SEQS];   // key-range splits of each of the sequence's query tiles
+  int ustart[AP_MAX_SEQS];   // first CTA of the levels that sequences 0..i share
+  int sbase[AP_MAX_SEQS];    // first partial result of a split sequence
+  int cbase[AP_MAX_SEQS];    // first combining CTA of a split sequence
+};
+struct PackedAttnParams {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* o;
+  int ldq, ldk, ldv, ldo;
+  int q_rows, k_rows, heads, kv_heads;
+  float sm_scale;
+  void* scratch;          // packed_plan_bytes() of device scratch (null if 0)
+  int* status;
+};
+void packed_plan(const int32_t* spans, int n, int heads, int kv_heads, int num_sms, PackedPlan* plan);
+size_t packed_plan_bytes(const PackedPlan& plan);
+int launch_attention_packed(const PackedAttnParams& p, const PackedPlan& plan, cudaStream_t st);
 
 }  // namespace qi

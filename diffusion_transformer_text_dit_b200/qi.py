@@ -30,6 +30,8 @@ QI_F32, QI_BF16 = 0, 1
 QI_EPI_STORE, QI_EPI_GELU_TANH, QI_EPI_GATED_RESIDUAL, QI_EPI_QKV_NORM_ROPE = 0, 1, 2, 3
 QI_KV_NONE, QI_KV_WRITE_PREFIX, QI_KV_READ_PREFIX = 0, 1, 2
 QI_MAX_GROUPS = 16
+QI_MAX_SEQS = 256
+QI_ACT_NONE, QI_ACT_GELU_TANH, QI_ACT_SILU = 0, 1, 2
 
 
 class QiError(RuntimeError):
@@ -52,6 +54,11 @@ class qi_w8(C.Structure):
 
 class qi_linear_bf16(C.Structure):
     _fields_ = [("w", C.c_void_p), ("bias", C.c_void_p), ("n", C.c_int32), ("k", C.c_int32)]
+
+
+class qi_gated_ffn(C.Structure):
+    _fields_ = [("gate", C.c_void_p), ("up", C.c_void_p), ("down", C.c_void_p),
+                ("hidden", C.c_int32), ("mlp", C.c_int32), ("act", C.c_int32)]
 
 
 class qi_epilogue(C.Structure):
@@ -134,6 +141,22 @@ _SIGS = {
     "qi_attn_block_causal_fp8": [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p,
                                  C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int,
                                  C.POINTER(qi_groups), C.c_float, C.c_void_p, C.c_int, C.c_void_p],
+    "qi_attn_causal_packed_workspace_bytes": [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int,
+                                              C.POINTER(C.c_size_t)],
+    "qi_attn_causal_packed": [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_int,
+                              C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int,
+                              C.c_void_p, C.c_int, C.c_float, C.c_void_p, C.c_int, C.c_void_p,
+                              C.c_size_t, C.c_void_p],
+    "qi_linear_act": [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.POINTER(qi_linear_bf16), C.c_int,
+                      C.c_void_p, C.c_int, C.c_void_p, C.c_int, C.c_void_p],
+    "qi_gated_ffn_workspace_bytes": [C.POINTER(qi_gated_ffn), C.c_int, C.c_int,
+                                     C.POINTER(C.c_size_t)],
+    "qi_gated_ffn_forward": [C.c_void_p, C.POINTER(qi_gated_ffn), C.c_void_p, C.c_int, C.c_int,
+                             C.c_void_p, C.c_int, C.c_void_p, C.c_int, C.c_void_p, C.c_void_p,
+                             C.c_size_t, C.c_void_p],
+    "qi_gated_ffn_backward": [C.c_void_p, C.POINTER(qi_gated_ffn), C.c_void_p, C.c_int, C.c_int,
+                              C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_int, C.c_void_p,
+                              C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p],
     "qi_to_e4m3": [C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p],
     "qi_attn_split_plan": [C.c_int, C.c_int, C.POINTER(qi_groups), C.c_int, C.c_size_t,
                            C.POINTER(C.c_int), C.POINTER(C.c_size_t)],
@@ -474,6 +497,180 @@ def qi_mxfp4_decode(ctx: Context, packed, scales, k: Optional[int] = None, out=N
     check(lib().qi_mxfp4_decode(ctx.handle, ptr(packed), ptr(scales), n, k_stored, k, ptr(out),
                                 stream_ptr(stream)))
     return out
+
+
+# Prompt-encoder layer.  These calls take bf16 matrices whose rows may be
+# strided (views of a fused q | k | v block, padded buffers).
+
+def _rows(ctx: Context, t: Optional[torch.Tensor], name: str, cols: int):
+    """(pointer, leading dimension) of a 2-D bf16 tensor on the context's device
+    with unit column stride."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda or t.device.index != ctx.device or t.dtype != torch.bfloat16 or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D bf16 tensor on cuda:{ctx.device}")
+    if t.shape[1] != cols:
+        raise ValueError(f"{name} has {t.shape[1]} columns, expected {cols}")
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if t.shape[0] <= 1:      # the distance between rows means nothing
+        return t.data_ptr(), cols
+    if ld < cols:
+        raise ValueError(f"{name} has overlapping rows")
+    return t.data_ptr(), ld
+
+
+def _new(shape, like: torch.Tensor, stream, dtype=torch.bfloat16):
+    """An output or workspace tensor, allocated on the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _on(ctx: Context, stream) -> int:
+    """Stream handle of a call: `stream`, or the current one of the context's device."""
+    return (stream if stream is not None else torch.cuda.current_stream(ctx.device)).cuda_stream
+
+
+def qi_attn_causal_packed_workspace_bytes(ctx: Context, spans: torch.Tensor, heads: int,
+                                          kv_heads: int) -> int:
+    n = C.c_size_t()
+    check(lib().qi_attn_causal_packed_workspace_bytes(ctx.handle, _spans(spans), spans.shape[0],
+                                                      heads, kv_heads, C.byref(n)))
+    return n.value
+
+
+def _spans(spans: torch.Tensor) -> int:
+    if spans.is_cuda or spans.dtype != torch.int32 or spans.dim() != 2 or spans.shape[1] != 4 \
+            or not spans.is_contiguous():
+        raise ValueError("spans must be a contiguous host int32 tensor [n, 4]")
+    return spans.data_ptr()
+
+
+def qi_attn_causal_packed(ctx: Context, q, k, v, spans: torch.Tensor, heads: int, kv_heads: int,
+                          sm_scale: Optional[float] = None, o: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention over packed sequences with grouped heads.  spans: host
+    int32 [n, 4] rows (first query row, queries, first key row, keys).  Rows of a
+    new o outside every sequence are not written."""
+    W, KW = heads * 128, kv_heads * 128
+    st = _on(ctx, stream)
+    if o is None:
+        o = _new((q.shape[0], W), q, stream)
+    if k.shape[0] != v.shape[0] or o.shape[0] != q.shape[0]:
+        raise ValueError("k and v, and q and o, must have the same number of rows")
+    qp, ldq = _rows(ctx, q, "q", W)
+    kp, ldk = _rows(ctx, k, "k", KW)
+    vp, ldv = _rows(ctx, v, "v", KW)
+    op, ldo = _rows(ctx, o, "o", W)
+    if workspace is None:
+        n = qi_attn_causal_packed_workspace_bytes(ctx, spans, heads, kv_heads)
+        if n:
+            workspace = _new(n, q, stream, torch.uint8)
+    check(lib().qi_attn_causal_packed(
+        ctx.handle, qp, ldq, q.shape[0], kp, ldk, vp, ldv, k.shape[0], heads, kv_heads, 128,
+        _spans(spans), spans.shape[0], sm_scale if sm_scale is not None else 128 ** -0.5, op, ldo,
+        ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0, st))
+    return o
+
+
+def qi_linear_act(ctx: Context, a: torch.Tensor, w: qi_linear_bf16, act: int = QI_ACT_NONE,
+                  residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                  stream=None):
+    """y = act(a w^T + bias) + residual, bf16 (residual may be y)."""
+    st = _on(ctx, stream)
+    M = a.shape[0]
+    if y is None:
+        y = _new((M, w.n), a, stream)
+    if y.shape[0] != M or (residual is not None and residual.shape[0] != M):
+        raise ValueError("a, residual and y must have the same number of rows")
+    ap, lda = _rows(ctx, a, "a", w.k)
+    rp, ldr = _rows(ctx, residual, "residual", w.n)
+    yp, ldy = _rows(ctx, y, "y", w.n)
+    check(lib().qi_linear_act(ctx.handle, ap, M, lda, C.byref(w), act, rp, ldr, yp, ldy, st))
+    return y
+
+
+def gated_ffn_struct(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
+                     act: int = QI_ACT_SILU) -> qi_gated_ffn:
+    """Weights of a gated feed-forward block: gate, up [mlp, hidden], down [hidden, mlp] bf16."""
+    F, H = gate.shape
+    if tuple(up.shape) != (F, H) or tuple(down.shape) != (H, F):
+        raise ValueError("gate and up must be [mlp, hidden], down [hidden, mlp]")
+    if any(t.dtype != torch.bfloat16 for t in (gate, up, down)):
+        raise ValueError("gated ffn weights must be bf16")
+    s = qi_gated_ffn()
+    s.gate, s.up, s.down, s.hidden, s.mlp, s.act = ptr(gate), ptr(up), ptr(down), H, F, act
+    s._keep = (gate, up, down)
+    return s
+
+
+def qi_gated_ffn_workspace_bytes(w: qi_gated_ffn, M: int, backward: bool = False) -> int:
+    n = C.c_size_t()
+    check(lib().qi_gated_ffn_workspace_bytes(C.byref(w), M, 1 if backward else 0, C.byref(n)))
+    return n.value
+
+
+def qi_gated_ffn_forward(ctx: Context, w: qi_gated_ffn, x: torch.Tensor,
+                         residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                         save: bool = False, gate_up: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None):
+    """y = (act(x gate^T) * (x up^T)) down^T + residual.  save=True (or a gate_up
+    buffer [M, 2 mlp]) also returns what the backward call needs: (y, gate_up)."""
+    st = _on(ctx, stream)
+    M = x.shape[0]
+    if y is None:
+        y = _new((M, w.hidden), x, stream)
+    if y.shape[0] != M or (residual is not None and residual.shape[0] != M):
+        raise ValueError("x, residual and y must have the same number of rows")
+    if save and gate_up is None:
+        gate_up = _new((M, 2 * w.mlp), x, stream)
+    if gate_up is not None and (tuple(gate_up.shape) != (M, 2 * w.mlp) or not gate_up.is_contiguous()
+                                or gate_up.dtype != torch.bfloat16):
+        raise ValueError("gate_up must be a contiguous bf16 tensor [M, 2 mlp]")
+    if workspace is None:
+        workspace = _new(qi_gated_ffn_workspace_bytes(w, M), x, stream, torch.uint8)
+    xp, ldx = _rows(ctx, x, "x", w.hidden)
+    rp, ldr = _rows(ctx, residual, "residual", w.hidden)
+    yp, ldy = _rows(ctx, y, "y", w.hidden)
+    check(lib().qi_gated_ffn_forward(ctx.handle, C.byref(w), xp, M, ldx, rp, ldr, yp, ldy,
+                                     ptr(gate_up), ptr(workspace), workspace.numel(), st))
+    return (y, gate_up) if gate_up is not None else y
+
+
+def qi_gated_ffn_backward(ctx: Context, w: qi_gated_ffn, x: torch.Tensor, dy: torch.Tensor,
+                          gate_up: torch.Tensor, dx: Optional[torch.Tensor] = None,
+                          dgate: Optional[torch.Tensor] = None, dup: Optional[torch.Tensor] = None,
+                          ddown: Optional[torch.Tensor] = None, want=("dx", "dgate", "dup", "ddown"),
+                          workspace: Optional[torch.Tensor] = None, stream=None):
+    """(dx, dgate, dup, ddown) of the block for the output gradient dy; gradients not
+    in `want` are not computed and come back as None."""
+    st = _on(ctx, stream)
+    M, H, F = x.shape[0], w.hidden, w.mlp
+    if dy.shape[0] != M or tuple(gate_up.shape) != (M, 2 * F) or gate_up.dtype != torch.bfloat16:
+        raise ValueError("dy must have x's rows and gate_up be [M, 2 mlp] bf16")
+    out = {}
+    for name, t, shape in (("dx", dx, (M, H)), ("dgate", dgate, (F, H)), ("dup", dup, (F, H)),
+                           ("ddown", ddown, (H, F))):
+        if name not in want:
+            out[name] = None
+            continue
+        if t is None:
+            t = _new(shape, x, stream)
+        if tuple(t.shape) != shape or t.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be bf16 {shape}")
+        out[name] = t
+    if workspace is None:
+        workspace = _new(qi_gated_ffn_workspace_bytes(w, M, True), x, stream, torch.uint8)
+    xp, ldx = _rows(ctx, x, "x", H)
+    dp, ldd = _rows(ctx, dy, "dy", H)
+    op, ldo = _rows(ctx, out["dx"], "dx", H)
+    check(lib().qi_gated_ffn_backward(ctx.handle, C.byref(w), xp, M, ldx, dp, ldd, ptr(gate_up), op,
+                                      ldo, ptr(out["dgate"]), ptr(out["dup"]), ptr(out["ddown"]),
+                                      ptr(workspace), workspace.numel(), st))
+    return out["dx"], out["dgate"], out["dup"], out["ddown"]
 
 
 def dims_struct(hidden, heads, mlp, patch, blocks, eps=1e-6) -> qi_dims:

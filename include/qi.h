@@ -357,6 +357,105 @@ int qi_attn_block_causal(qi_ctx* ctx, const uint16_t* q, int ldq, int Sq, int q_
 int qi_attn_split_plan(int Sk, int heads, const qi_groups* groups, int num_sms,
                        size_t scratch_bytes, int* split_heads, size_t* bytes);
 
+/* ------------------------------------------------------------------ prompt-encoder layer
+ *
+ * The operators that a layer of the prompt encoder is made of ([GC] Graph
+ * contracts: txt_feats [1, L, 4096], the encoder's last hidden state, is the
+ * text input of a step).  With rows x of several packed prompts:
+ *   qkv = qi_linear_act(x);  o = qi_attn_causal_packed(q, k, v);
+ *   x   = qi_linear_act(o) + x;  x = qi_gated_ffn_forward(x) + x
+ * (norms and rotary embedding in between).  The pages describe no such call.
+ * These calls work whichever device is current (the context's is made current
+ * for the call and the former one restored), use no state of the context other
+ * than its status word and launch counters, and may be captured into a CUDA
+ * graph.  Two calls may run at the same time on different streams, from
+ * different contexts if from different host threads, as long as their
+ * outputs and workspaces are different memory.  An
+ * output must not overlap an input or the workspace unless the call says so. */
+
+/* Causal attention over packed sequences with grouped heads:
+ *   O = softmax(Q K^T sm_scale + mask) V per head; query head h uses key/value
+ *   head h / (heads / kv_heads).
+ * q [q_rows, ldq], o [q_rows, ldo], k [k_rows, ldk], v [k_rows, ldv] bf16; query
+ * head h is columns [h*128, (h+1)*128) of q and o, key/value head likewise, so
+ * the parts of one fused q | k | v row block can be passed with its ld.
+ * spans: HOST int32 table [n_seqs][4] of (first query row, queries, first key
+ * row, keys), 0 <= n_seqs <= QI_MAX_SEQS, read before the call returns.  Query
+ * i of a sequence with ql queries and kl keys sees its keys 0 .. kl - ql + i:
+ * kl = ql is a whole prompt, kl > ql a prompt (or with ql = 1 a single token)
+ * behind kl - ql cached keys.  A query that sees no key (kl - ql + i < 0) gets
+ * zeros.  Sequences may be empty, must not share query rows and may share key
+ * rows; rows of o outside every sequence are left as they were, and key rows
+ * outside a sequence have no effect on it, whatever they hold.  A key that a
+ * query may not see has weight 0 in that query's sum; inside its own sequence
+ * its value must be finite (0 * infinity is NaN).
+ * head_dim must be 128; heads a multiple of kv_heads, heads / kv_heads <= 128;
+ * leading dimensions multiples of 8; sm_scale > 0.  workspace: of the size the
+ * function below returns for the same table (0 for most: only sequences whose
+ * keys are many and queries few are split over their keys), contents
+ * irrelevant.  Scores, maxima, sums and O are fp32; the weights enter P V as bf16.
+ * The result of a sequence depends on the table only through the split of its
+ * key range (rounding). */
+#define QI_MAX_SEQS 256
+int qi_attn_causal_packed_workspace_bytes(qi_ctx* ctx, const int32_t* spans, int n_seqs, int heads,
+                                          int kv_heads, size_t* bytes);
+int qi_attn_causal_packed(qi_ctx* ctx, const uint16_t* q, int ldq, int q_rows, const uint16_t* k,
+                          int ldk, const uint16_t* v, int ldv, int k_rows, int heads, int kv_heads,
+                          int head_dim, const int32_t* spans, int n_seqs, float sm_scale,
+                          uint16_t* o, int ldo, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+typedef enum {
+  QI_ACT_NONE = 0,
+  QI_ACT_GELU_TANH = 1,   /* 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+  QI_ACT_SILU = 2         /* x / (1 + e^-x) */
+} qi_act;
+
+/* BF16 Linear with bias, activation and residual in its epilogue:
+ *   y [M, w.n] bf16 (ld ldy) = bf16(act(a [M, w.k] W^T + bias) + residual [M, w.n])
+ * fp32 until the one rounding at the end.  residual may be NULL, or y itself
+ * (same pointer and ld: y is updated in place).  Any n >= 1 and any ldy,
+ * ld_residual >= n (rows that are 16-byte aligned are written faster); k and
+ * lda multiples of 8; a, W and bias 16-byte aligned. */
+int qi_linear_act(qi_ctx* ctx, const uint16_t* a, int M, int lda, const qi_linear_bf16* w, int act,
+                  const uint16_t* residual, int ld_residual, uint16_t* y, int ldy, void* stream);
+
+/* Gated feed-forward block: y = (act(x Wg^T) * (x Wu^T)) Wd^T. */
+typedef struct qi_gated_ffn {
+  const uint16_t* gate;   /* [mlp, hidden] bf16 */
+  const uint16_t* up;     /* [mlp, hidden] bf16 */
+  const uint16_t* down;   /* [hidden, mlp] bf16 */
+  int32_t hidden, mlp;    /* multiples of 8 */
+  int32_t act;            /* QI_ACT_SILU or QI_ACT_GELU_TANH */
+} qi_gated_ffn;
+
+/* Workspace bytes of the forward (backward == 0) or the backward call for M rows. */
+int qi_gated_ffn_workspace_bytes(const qi_gated_ffn* w, int M, int backward, size_t* bytes);
+
+/* h = bf16(act(x Wg^T) * (x Wu^T)) (both projections, activation and product in
+ * one kernel, fp32 inside), y [M, hidden] = bf16(h Wd^T + residual).
+ * residual: NULL, or rows added before the rounding; residual == y (same ld)
+ * and y == x are allowed.  gate_up: NULL, or [M, 2 mlp] bf16 that receives
+ * x Wg^T | x Wu^T for the backward call. */
+int qi_gated_ffn_forward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x, int M, int ldx,
+                         const uint16_t* residual, int ld_residual, uint16_t* y, int ldy,
+                         uint16_t* gate_up, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of sum(dy * y) for the block above (the residual's is dy itself):
+ *   dh = dy Wd; dg = dh u act'(g); du = dh act(g); h = act(g) u
+ *   dx = dg Wg + du Wu; dgate = dg^T x; dup = du^T x; ddown = dy^T h
+ * g | u = gate_up from the forward call, the same x and weights.  dg, du and h
+ * are rounded to bf16 as operands of the products that follow; every sum is
+ * fp32 and every gradient is rounded to bf16 once.  Each of dx [M, hidden],
+ * dgate, dup [mlp, hidden], ddown [hidden, mlp] may be NULL (not wanted); the
+ * others are overwritten, in the same bits on every call (no atomics).  With
+ * M = 0 the weights' gradients are set to 0.  A row of dy, x or gate_up whose
+ * values are not finite makes the weights' gradients not finite. */
+int qi_gated_ffn_backward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x, int M, int ldx,
+                          const uint16_t* dy, int ld_dy, const uint16_t* gate_up, uint16_t* dx,
+                          int ld_dx, uint16_t* dgate, uint16_t* dup, uint16_t* ddown,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------------ block */
 
 /* Block-causal attention with e4m3 operands (the pages' reduced-precision
