@@ -29,9 +29,13 @@
 // steps that hold a visible key, and the producer warp clears the rows between
 // the last visible key and the end of its step.
 //
-// Few rows and many keys (single tokens): the key range of a tile is split
-// over nsp CTAs, which write unnormalised O, maximum and sum to scratch; a
-// second kernel joins them in a fixed order.
+// Few rows (single tokens: ql G <= AT_MAX_ROWS) leave such a tile almost empty
+// and are bound by reading the keys once; they run in a second kernel that
+// feeds warp-level MMAs straight from memory (ap_token_kernel).
+//
+// Few rows and many keys: the key range of a tile is split over nsp CTAs,
+// which write unnormalised O, maximum and sum to scratch; a third kernel
+// joins them in a fixed order.
 #include <string.h>
 
 #include <algorithm>
@@ -54,8 +58,11 @@ constexpr int AP_SMEM = 1024 + (2 + AP_KST + AP_VST) * AP_TILE + 256;
 
 struct ApKernelParams {
   PackedPlan plan;
+  const uint16_t* q;   // for the token kernel (the tile kernel reads it through a tensor map)
+  int ldq;
   uint16_t* o;
-  int ldo, heads, kv_heads;
+  int ldo, kv_heads;
+  int row_blocks;    // token kernel: 16-row blocks per unit
   float sm_scale;
   float* part_o;     // [slots][slot_rows][128]
   float* part_ml;    // [slots][slot_rows][2]
@@ -71,30 +78,30 @@ struct ApUnit {
 };
 __host__ __device__ __forceinline__ int ap_tiles(const PackedPlan& d, int s) {
   const int per = d.P * d.nq;
-  return (d.ql[s] + per - 1) / per;
+  return (d.seq[s].ql + per - 1) / per;
 }
 __host__ __device__ __forceinline__ ApUnit ap_unit(const PackedPlan& d, int kv_heads, int b) {
   // ustart falls with i: the levels shared by sequences 0..i begin at ustart[i]
   int lo = 0, hi = d.n_seqs - 1;
   while (lo < hi) {   // the first i whose levels begin at or before b
     const int mid = (lo + hi) >> 1;
-    if (d.ustart[mid] <= b) hi = mid;
+    if (d.seq[mid].ustart <= b) hi = mid;
     else lo = mid + 1;
   }
   const int per_level = (lo + 1) * kv_heads;
-  const int e0 = lo + 1 < d.n_seqs ? ap_tiles(d, lo + 1) * d.nsp[lo + 1] : 0;
-  const int r = b - d.ustart[lo];
+  const int e0 = lo + 1 < d.n_seqs ? ap_tiles(d, lo + 1) * d.seq[lo + 1].nsp : 0;
+  const int r = b - d.seq[lo].ustart;
   const int e = e0 + r / per_level, w = r % per_level;
   ApUnit u;
   u.s = w / kv_heads;
   u.h = w - u.s * kv_heads;
-  const int nsp = d.nsp[u.s];
+  const int nsp = d.seq[u.s].nsp;
   u.ct = ap_tiles(d, u.s) - 1 - e / nsp;
   u.j = e % nsp;
   return u;
 }
 __host__ __device__ __forceinline__ int ap_slot(const PackedPlan& d, int kv_heads, int s, int ct, int h, int j) {
-  return d.sbase[s] + (ct * d.nsp[s] + j) * kv_heads + h;
+  return d.seq[s].sbase + (ct * d.seq[s].nsp + j) * kv_heads + h;
 }
 
 __device__ __forceinline__ void ap_softmax_bar() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -106,6 +113,14 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// Ask for a tile in L2.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
 }
 
 __global__ void __launch_bounds__(AP_THREADS, 1)
@@ -137,7 +152,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const ApUnit u = ap_unit(d, p.kv_heads, static_cast<int>(blockIdx.x));
   const int G = d.G, P = d.P, nq = d.nq;
-  const int ql = d.ql[u.s], kl = d.kl[u.s], k0s = d.k0[u.s], nsp = d.nsp[u.s];
+  const int ql = d.seq[u.s].ql, kl = d.seq[u.s].kl, k0s = d.seq[u.s].k0, nsp = d.seq[u.s].nsp;
   const int p0 = u.ct * P * nq;                    // first query position of this CTA
   const int first = kl - ql + 1;                   // keys that query position 0 sees (may be negative)
   // keys that the last position of tile X sees, and its key tiles
@@ -204,7 +219,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       for (int t = 0; t < nq; ++t)
         for (int half = 0; half < 2; ++half)
           tma_load_3d(&tmQ, q_full, sQ + t * AP_TILE + half * AP_HALF, 64 * half, u.h * G,
-                      d.q0[u.s] + p0 + t * P);
+                      d.seq[u.s].q0 + p0 + t * P);
       int jk = 0, jv = 0;   // tiles whose loads were issued
       for (int j = 0; j < n_kv; ++j) {
         const int row = k0s + (lo + j) * AP_ROWS;
@@ -473,7 +488,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         const int tr = quarter * 32 + rr, ps = p0 + X * P + tr / G;
         if (tr < P * G && ps < ql) {
           const uint4 w = *reinterpret_cast<const uint4*>(rows + rr * 256 + ((x ^ (rr & 15)) << 4));
-          *reinterpret_cast<uint4*>(p.o + static_cast<size_t>(d.q0[u.s] + ps) * p.ldo +
+          *reinterpret_cast<uint4*>(p.o + static_cast<size_t>(d.seq[u.s].q0 + ps) * p.ldo +
                                     (u.h * G + tr % G) * 128 + x * 8) = w;
         }
       }
@@ -488,138 +503,494 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
   }
 }
 
-// Join the key ranges of a split tile: with m = max m_j over the ranges that
-// have weight, O = sum O_j 2^(m_j - m) / sum l_j 2^(m_j - m), j ascending.
-// One CTA per (sequence, query tile group, key/value head); 32 lanes cover a
-// row's 128 columns.
-constexpr int AP_JOIN_THREADS = 256;
-__global__ void __launch_bounds__(AP_JOIN_THREADS) ap_join_kernel(const __grid_constant__ ApKernelParams p) {
+// ---------------------------------------------------------------- few rows
+//
+// A unit of work is 16 rows (query heads of one key/value head, at one or more
+// positions) over a range of keys.  A producer thread streams the keys with
+// TMA, 64 at a time, through a ring of stages deep enough to keep the memory
+// busy (two CTAs per SM hold 192 KB in flight) and runs ahead into the CTA's
+// next units; each of four warps takes 16 keys of a stage with its own
+// running maximum, sum and O (m16n8k16 MMAs, K and V fragments by ldmatrix
+// from the swizzled tile), and the warps are joined at the unit's end in
+// shared memory.  A 128-row tcgen05 tile would be almost empty here, and its
+// fixed steps (TMEM, the S / P round trip) longer than the loads.  Before it
+// waits for the previous kernel of the stream, a CTA asks for the keys of its
+// first unit in L2 (no value is read then, so nothing stale is seen).
+constexpr int AT_WARPS = 4;
+constexpr int AT_THREADS = 32 * (AT_WARPS + 1);
+constexpr int AT_MAX_ROWS = 32;
+constexpr int AT_KEYS = 64;                        // keys of a stage
+constexpr int AT_STAGES = 3;
+constexpr int AT_HALF = AT_KEYS * 128;             // bytes of one 64-column half of K or V
+constexpr int AT_STAGE = 4 * AT_HALF;              // K | V, two halves each
+constexpr int AT_SMEM = 1024 + AT_STAGES * AT_STAGE + 128;
+static_assert(AT_WARPS * 16 == AT_KEYS, "a warp takes 16 keys of a stage");
+
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// Named barrier over the compute warps: plain, and with an AND of a predicate.
+__device__ __forceinline__ void at_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool at_all(bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(pred))
+      : "memory");
+  return r != 0;
+}
+
+__global__ void __launch_bounds__(AT_THREADS, 2)
+    ap_token_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ ApKernelParams p) {
   const PackedPlan& d = p.plan;
-  const int b = static_cast<int>(blockIdx.x);
-  int s = 0;
-  while (!(d.nsp[s] > 1 && b >= d.cbase[s] && b < d.cbase[s] + ap_tiles(d, s) * p.kv_heads)) {
-    if (s == d.n_seqs - 1) return;
-    ++s;
+  int* status = p.status;
+  __shared__ float s_ml[AT_WARPS][16][2];
+  __shared__ float s_o[AT_WARPS][4][128];
+  extern __shared__ uint8_t at_smem_raw[];
+  const uint32_t raw_addr = smem_u32(at_smem_raw);
+  uint8_t* smem = at_smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + AT_STAGES * AT_STAGE);   // [AT_STAGES]
+  uint64_t* empty = full + AT_STAGES;                                          // [AT_STAGES]
+  const int G = d.G, total = d.units * p.row_blocks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < AT_STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], AT_WARPS);
+    }
+    fence_mbar_init();
   }
-  const int ct = (b - d.cbase[s]) / p.kv_heads, h = (b - d.cbase[s]) % p.kv_heads;
-  const int G = d.G, nsp = d.nsp[s], p0 = ct * d.P * d.nq;
-  const int rows = min(d.P * d.nq, d.ql[s] - p0) * G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __syncthreads();
+
+  // The units of this CTA: one of every gridDim.x, alternately from the front
+  // and the back of each round, so that longest-first order evens out.
+  auto unit_of = [&](int round) {
+    const int n = static_cast<int>(gridDim.x), i = static_cast<int>(blockIdx.x);
+    return round * n + ((round & 1) ? n - 1 - i : i);
+  };
+  struct Work {
+    ApUnit u;
+    int r0, rows, lo, hi;   // first of 16 rows, rows of the unit, 64-key steps
+  };
+  auto work_of = [&](int w) {
+    Work x;
+    x.u = ap_unit(d, p.kv_heads, w / p.row_blocks);
+    x.r0 = w % p.row_blocks * 16;
+    x.rows = d.seq[x.u.s].ql * G;
+    const int nsp = d.seq[x.u.s].nsp, steps = x.r0 < x.rows ? (d.seq[x.u.s].kl + AT_KEYS - 1) / AT_KEYS : 0;
+    x.lo = static_cast<int>(static_cast<long long>(steps) * x.u.j / nsp);
+    x.hi = static_cast<int>(static_cast<long long>(steps) * (x.u.j + 1) / nsp);
+    return x;
+  };
+
+  if (warp == AT_WARPS) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+      if (unit_of(0) < total) {
+        const Work w = work_of(unit_of(0));
+        for (int st = w.lo; st < w.hi; ++st)
+          for (int half = 0; half < 2; ++half) {
+            tma_prefetch_2d(&tmK, w.u.h * 128 + 64 * half, d.seq[w.u.s].k0 + st * AT_KEYS);
+            tma_prefetch_2d(&tmV, w.u.h * 128 + 64 * half, d.seq[w.u.s].k0 + st * AT_KEYS);
+          }
+      }
+    }
+    pdl_wait();
+    pdl_trigger();
+    if (lane == 0) {
+      bool ok = true;
+      int i = 0;   // steps loaded, over all units
+      for (int round = 0; ok && unit_of(round) < total; ++round) {
+        const Work w = work_of(unit_of(round));
+        for (int st = w.lo; st < w.hi; ++st, ++i) {
+          const int sl = i % AT_STAGES;
+          if (!mbar_wait(&empty[sl], ((i / AT_STAGES) & 1) ^ 1u, status)) { ok = false; break; }
+          mbar_arrive_expect_tx(&full[sl], AT_STAGE);
+          uint8_t* dst = smem + sl * AT_STAGE;
+          const int row = d.seq[w.u.s].k0 + st * AT_KEYS;
+          for (int half = 0; half < 2; ++half) {
+            tma_load_2d(&tmK, &full[sl], dst + half * AT_HALF, w.u.h * 128 + 64 * half, row);
+            tma_load_2d(&tmV, &full[sl], dst + (2 + half) * AT_HALF, w.u.h * 128 + 64 * half, row);
+          }
+        }
+      }
+      if (!ok) {   // bounded drain of the loads already armed
+        for (int k = max(0, i - AT_STAGES); k < i; ++k) {
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(&full[k % AT_STAGES], (k / AT_STAGES) & 1) && globaltimer_ns() - t0 < QI_WAIT_NS) {
+          }
+        }
+      }
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- compute warps
+  Work w = work_of(min(unit_of(0), total - 1));
   pdl_wait();
   pdl_trigger();
-  for (int r = warp; r < rows; r += AP_JOIN_THREADS / 32) {
-    const size_t step = static_cast<size_t>(p.kv_heads) * d.slot_rows;
-    const size_t at = static_cast<size_t>(ap_slot(d, p.kv_heads, s, ct, h, 0)) * d.slot_rows + r;
-    float m = -INFINITY;
-    for (int j = lane; j < nsp; j += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (at + j * step));
-      if (ml.y != 0.f) m = fmaxf(m, ml.x);   // NaN sums count too
-    }
+  const float sl2 = p.sm_scale * 1.4426950408889634f;
+  // ldmatrix row addresses: lane gives row (lane & 7) of matrix lane >> 3.
+  // K: matrices (keys 0-7, 8-15) x (columns 0-7, 8-15 of a 16-column step)
+  // V: matrices (keys 0-7, 8-15) x (two 8-column groups)
+  const int mrow = warp * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, mcol = lane >> 4;
+  int i = 0;   // steps taken, over all units
+  for (int round = 0; unit_of(round) < total; ++round) {
+    if (round > 0) w = work_of(unit_of(round));
+    const PackedPlan::Seq& sq = d.seq[w.u.s];
+    const int ql = sq.ql, kl = sq.kl, nsp = sq.nsp, r0 = w.r0, rows = w.rows;
+    if (r0 >= rows) continue;
+    uint32_t qa[8][4];   // A fragments of 16 head columns each
+    int lim[2];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float lsum = 0.f;
-#pragma unroll 4
-    for (int j = 0; j < nsp; ++j) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (at + j * step));
-      if (ml.y == 0.f) continue;   // no key of this range is visible: O_j may be unwritten
-      const float f = exp2f(ml.x - m);
-      const float4 o = *reinterpret_cast<const float4*>(p.part_o + (at + j * step) * 128 + lane * 4);
-      acc.x = fmaf(o.x, f, acc.x);
-      acc.y = fmaf(o.y, f, acc.y);
-      acc.z = fmaf(o.z, f, acc.z);
-      acc.w = fmaf(o.w, f, acc.w);
-      lsum = fmaf(ml.y, f, lsum);
+    for (int e = 0; e < 2; ++e) {
+      const int r = r0 + g + 8 * e;
+      const bool live = r < rows;
+      lim[e] = live ? max(0, kl - ql + r / G + 1) : 0;   // keys the row sees
+      const uint16_t* row = p.q + static_cast<size_t>(sq.q0 + (live ? r / G : 0)) * p.ldq +
+                            (w.u.h * G + r % G) * 128 + 2 * t;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        qa[kk][e] = live ? *reinterpret_cast<const uint32_t*>(row + 16 * kk) : 0u;
+        qa[kk][2 + e] = live ? *reinterpret_cast<const uint32_t*>(row + 16 * kk + 8) : 0u;
+      }
     }
-    const float inv = lsum == 0.f ? 0.f : 1.0f / lsum;
-    const uint2 w = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    *reinterpret_cast<uint2*>(p.o + static_cast<size_t>(d.q0[s] + p0 + r / G) * p.ldo +
-                              (h * G + r % G) * 128 + lane * 4) = w;
+    const int lim_min = max(0, kl - ql + r0 / G + 1);   // keys that every row sees
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // rows g, g + 8; m: base-2 scaled reference
+    float o[16][4];   // head columns 8 c + 2 t, + 1 of rows g and g + 8
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
+    bool ok = true;
+#pragma unroll 1
+    for (int st = w.lo; st < w.hi; ++st, ++i) {
+      const int sl = i % AT_STAGES;
+      if (!mbar_wait_warp(&full[sl], (i / AT_STAGES) & 1, status)) { ok = false; break; }
+      uint8_t* stage = smem + sl * AT_STAGE;
+      const int key0 = st * AT_KEYS + warp * 16;
+      if (key0 < kl) {
+        if (key0 + 16 > kl) {
+          // rows behind the last key: weight 0, but whatever they hold must not be multiplied
+          for (int x = lane; x < (key0 + 16 - kl) * 16; x += 32)
+            *reinterpret_cast<uint4*>(stage + (2 + ((x >> 3) & 1)) * AT_HALF + (kl - st * AT_KEYS + (x >> 4)) * 128 +
+                                      (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();   // before TMA writes the stage again
+          __syncwarp();
+        }
+        const uint32_t kbase = smem_u32(stage) + mrow * 128, vbase = kbase + 2 * AT_HALF;
+        float s[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const int chunk = (kk & 3) * 2 + mcol;   // 16-byte chunk of the 128-byte row, swizzled
+          uint32_t b[4];                           // keys 0-7 | 8-15 at columns 0-7, then at 8-15
+          ldsm_x4(b, kbase + (kk >> 2) * AT_HALF + ((chunk ^ (mrow & 7)) << 4));
+          mma_16816(s[0], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[0], b[2]);
+          mma_16816(s[1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[1], b[3]);
+        }
+        if (key0 + 16 > lim_min) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key0 + 8 * n + 2 * t + (e & 1) >= lim[e >> 1]) s[n][e] = -INFINITY;
+        }
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2)) * sl2;
+          // the reference moves only when the maximum exceeds it by more than 8 (P <= 256)
+          f[e] = 1.f;
+          if (x > m[e] + 8.f || m[e] == -INFINITY) {
+            f[e] = m[e] == -INFINITY ? 1.f : exp2f(m[e] - x);   // no key seen yet: O and l are 0
+            m[e] = x;
+          }
+        }
+        if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) l[e] *= f[e];
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[c][e] *= f[e >> 1];
+        }
+        uint32_t pa[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float ref = m[e] == -INFINITY ? 0.f : m[e];
+            const float x0 = ex2_approx(fmaf(s[n][2 * e], sl2, -ref)), x1 = ex2_approx(fmaf(s[n][2 * e + 1], sl2, -ref));
+            l[e] += x0 + x1;
+            pa[2 * n + e] = pack_bf16x2(x0, x1);
+          }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {   // 16 head columns: two 8-column products
+          const int chunk = (c & 3) * 2 + mcol;
+          uint32_t b[4];
+          ldsm_x4_trans(b, vbase + (c >> 2) * AT_HALF + ((chunk ^ (mrow & 7)) << 4));
+          mma_16816(o[2 * c], pa[0], pa[1], pa[2], pa[3], b[0], b[1]);
+          mma_16816(o[2 * c + 1], pa[0], pa[1], pa[2], pa[3], b[2], b[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[sl]);
+    }
+    // join the warps: m = max over those that saw a key
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      if (t == 0) {
+        s_ml[warp][g + 8 * e][0] = m[e];
+        s_ml[warp][g + 8 * e][1] = l[e];
+      }
+    }
+    if (!at_all(ok)) return;
+    float f[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < AT_WARPS; ++x) mx = fmaxf(mx, s_ml[x][g + 8 * e][0]);
+      f[e] = m[e] == -INFINITY ? 0.f : exp2f(m[e] - mx);
+    }
+    const int n_rows = min(16, rows - r0), col = threadIdx.x;
+    const size_t slot = nsp > 1 ? static_cast<size_t>(ap_slot(d, p.kv_heads, w.u.s, 0, w.u.h, w.u.j)) * d.slot_rows + r0 : 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {   // four rows at a time
+      if (4 * b >= n_rows) break;
+      if ((g >> 2) == (b & 1)) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          *reinterpret_cast<float2*>(&s_o[warp][g & 3][8 * c + 2 * t]) =
+              make_float2(o[c][2 * (b >> 1)] * f[b >> 1], o[c][2 * (b >> 1) + 1] * f[b >> 1]);
+      }
+      at_bar();
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int r = 4 * b + x;
+        if (r >= n_rows) break;
+        float mx = -INFINITY, sum = 0.f, v = 0.f;
+#pragma unroll
+        for (int y = 0; y < AT_WARPS; ++y) mx = fmaxf(mx, s_ml[y][r][0]);
+#pragma unroll
+        for (int y = 0; y < AT_WARPS; ++y) {
+          const float my = s_ml[y][r][0];
+          if (my == -INFINITY && s_ml[y][r][1] == 0.f) continue;   // saw no key
+          sum = fmaf(s_ml[y][r][1], exp2f(my - mx), sum);
+          v += s_o[y][x][col];
+        }
+        if (nsp > 1) {
+          p.part_o[(slot + r) * 128 + col] = v;
+          if (col == 0) {
+            p.part_ml[2 * (slot + r)] = mx;
+            p.part_ml[2 * (slot + r) + 1] = sum;
+          }
+        } else {
+          const int row = r0 + r;
+          v = sum == 0.f ? 0.f : v / sum;
+          p.o[static_cast<size_t>(sq.q0 + row / G) * p.ldo + (w.u.h * G + row % G) * 128 + col] =
+              static_cast<uint16_t>(pack_bf16x2(v, 0.f));
+        }
+      }
+      at_bar();   // s_o and, after the last rows, s_ml may be written again
+    }
   }
+}
+
+// Join the key ranges of a split tile: with m = max m_j over the ranges that
+// have weight, O = sum O_j 2^(m_j - m) / sum l_j 2^(m_j - m), always in the
+// same order.  One CTA per row: warp w adds ranges w, w + 4, ..., 32 lanes
+// cover the 128 columns, and the four sums are added in shared memory.
+constexpr int AP_JOIN_WARPS = 4;
+__global__ void __launch_bounds__(32 * AP_JOIN_WARPS) ap_join_kernel(const __grid_constant__ ApKernelParams p) {
+  const PackedPlan& d = p.plan;
+  __shared__ float4 s_o[AP_JOIN_WARPS][32];
+  __shared__ float s_l[AP_JOIN_WARPS];
+  const int b = static_cast<int>(blockIdx.x), r = static_cast<int>(blockIdx.y);
+  // the last sequence whose groups begin at or before b (an unsplit one has none and begins
+  // where the next split one does)
+  int s = 0, s_hi = d.n_seqs - 1;
+  while (s < s_hi) {
+    const int mid = (s + s_hi + 1) >> 1;
+    if (d.seq[mid].cbase <= b) s = mid;
+    else s_hi = mid - 1;
+  }
+  const int ct = (b - d.seq[s].cbase) / p.kv_heads, h = (b - d.seq[s].cbase) % p.kv_heads;
+  const int G = d.G, nsp = d.seq[s].nsp, p0 = ct * d.P * d.nq;
+  const int n_rows = min(d.P * d.nq, d.seq[s].ql - p0) * G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t step = static_cast<size_t>(p.kv_heads) * d.slot_rows;
+  const size_t at = static_cast<size_t>(ap_slot(d, p.kv_heads, s, ct, h, 0)) * d.slot_rows + r;
+  pdl_wait();   // (all of the above comes from the launch's own arguments)
+  pdl_trigger();
+  if (r >= n_rows) return;
+  float m = -INFINITY;
+  for (int j = lane; j < nsp; j += 32) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (at + j * step));
+    if (ml.y != 0.f) m = fmaxf(m, ml.x);   // NaN sums count too
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float lsum = 0.f;
+#pragma unroll 4
+  for (int j = warp; j < nsp; j += AP_JOIN_WARPS) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (at + j * step));
+    float4 o = *reinterpret_cast<const float4*>(p.part_o + (at + j * step) * 128 + lane * 4);
+    const bool none = ml.y == 0.f;   // no key of this range is visible: O_j may be unwritten
+    const float f = none ? 0.f : exp2f(ml.x - m);
+    if (none) o = make_float4(0.f, 0.f, 0.f, 0.f);
+    acc.x = fmaf(o.x, f, acc.x);
+    acc.y = fmaf(o.y, f, acc.y);
+    acc.z = fmaf(o.z, f, acc.z);
+    acc.w = fmaf(o.w, f, acc.w);
+    lsum = fmaf(ml.y, f, lsum);
+  }
+  s_o[warp][lane] = acc;
+  if (lane == 0) s_l[warp] = lsum;
+  __syncthreads();
+  if (warp > 0) return;
+#pragma unroll
+  for (int w = 1; w < AP_JOIN_WARPS; ++w) {
+    const float4 x = s_o[w][lane];
+    acc = make_float4(acc.x + x.x, acc.y + x.y, acc.z + x.z, acc.w + x.w);
+    lsum += s_l[w];
+  }
+  const float inv = lsum == 0.f ? 0.f : 1.0f / lsum;
+  const uint2 w = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  *reinterpret_cast<uint2*>(p.o + static_cast<size_t>(d.seq[s].q0 + p0 + r / G) * p.ldo +
+                            (h * G + r % G) * 128 + lane * 4) = w;
 }
 
 // ---------------------------------------------------------------- host side
 
-// Launch plan of a table of sequences: a pure function of its arguments.
-//  * nq = 2 (two query tiles share a CTA's key stream and hide each other's
-//    softmax) unless that leaves SMs without a CTA or every sequence has no
-//    more positions than one tile holds.
-//  * key ranges are split when the longest CTA would outlast the average load
-//    of an SM: ranges of about that average, at least AP_MIN_RANGE key tiles
-//    (a range costs a partial result and the joining kernel).
+// Launch plans of a table of sequences, one for the tile kernel and one for the
+// token kernel: a pure function of the arguments.
+//  * sequences of at most AT_MAX_ROWS rows go to the token kernel.
+//  * tile kernel: nq = 2 (two query tiles share a CTA's key stream and hide each
+//    other's softmax) unless that leaves SMs without a CTA or every sequence
+//    has no more positions than one tile holds; key ranges are split when the
+//    longest CTA would outlast the average load of an SM, into ranges of about
+//    that average, at least AP_MIN_RANGE key tiles (a range costs a partial
+//    result and the joining kernel).
+//  * token kernel: two CTAs fit on an SM; ranges are as long as gives every
+//    place one CTA, but between AT_MIN_KEYS (fewer keys do not pay for a
+//    partial result) and AT_MAX_KEYS (shorter CTAs even out ragged lengths).
 constexpr int AP_MIN_RANGE = 4;
+constexpr int AT_MIN_KEYS = 256, AT_MAX_KEYS = 512;
 
-void packed_plan(const int32_t* spans, int n, int heads, int kv_heads, int num_sms, PackedPlan* d) {
-  memset(d, 0, sizeof(*d));
-  d->G = heads / kv_heads;
-  d->P = AP_ROWS / d->G;
-  struct Seq {
-    int q0, ql, k0, kl, e, nsp;
-  };
-  std::vector<Seq> seq;
-  int max_ql = 0;
-  for (int i = 0; i < n; ++i) {
-    const int32_t* t = spans + 4 * i;
-    if (t[1] == 0) continue;
-    seq.push_back({t[0], t[1], t[2], t[3], 0, 1});
-    max_ql = std::max(max_ql, t[1]);
-  }
+struct PlanSeq {
+  int q0, ql, k0, kl, e, nsp;
+};
+
+// Launch order, partial results and CTA numbers of a plan whose nq and splits are chosen.
+static void plan_finish(std::vector<PlanSeq>& seq, int kv_heads, PackedPlan* d) {
   d->n_seqs = static_cast<int>(seq.size());
-  if (seq.empty()) return;
-  auto tiles = [&](const Seq& s, int nq) { return (s.ql + d->P * nq - 1) / (d->P * nq); };
-  auto key_tiles = [&](const Seq& s, int nq, int ct) {   // of query tile group ct
-    const long long end = static_cast<long long>(s.kl) - s.ql + std::min((ct + 1) * d->P * nq, s.ql);
-    return end > 0 ? (end + AP_ROWS - 1) / AP_ROWS : 0ll;
-  };
-  long long units2 = 0;
-  for (const Seq& s : seq) units2 += static_cast<long long>(tiles(s, 2)) * kv_heads;
-  d->nq = max_ql > d->P && units2 >= num_sms ? 2 : 1;
-  long long total = 0, longest = 0, units = 0;
-  for (const Seq& s : seq) {
-    const int t = tiles(s, d->nq);
-    units += static_cast<long long>(t) * kv_heads;
-    for (int c = 0; c < t; ++c) total += key_tiles(s, d->nq, c) * kv_heads;
-    longest = std::max(longest, key_tiles(s, d->nq, t - 1));
-  }
-  const long long share = (total + num_sms - 1) / num_sms;
-  const long long range = std::max<long long>(AP_MIN_RANGE, share);
-  if (longest >= 2 * range)
-    for (Seq& s : seq) {
-      const long long k = key_tiles(s, d->nq, tiles(s, d->nq) - 1);
-      if (k >= 2 * range) s.nsp = static_cast<int>((k + range - 1) / range);
-    }
-  for (Seq& s : seq) s.e = tiles(s, d->nq) * s.nsp;
-  std::stable_sort(seq.begin(), seq.end(), [](const Seq& a, const Seq& b) {
+  auto tiles = [&](const PlanSeq& s) { return (s.ql + d->P * d->nq - 1) / (d->P * d->nq); };
+  for (PlanSeq& s : seq) s.e = tiles(s) * s.nsp;
+  std::stable_sort(seq.begin(), seq.end(), [](const PlanSeq& a, const PlanSeq& b) {
     return a.e != b.e ? a.e > b.e : a.kl > b.kl;
   });
-  int rows = 0;
   for (int i = 0; i < d->n_seqs; ++i) {
-    const Seq& s = seq[i];
-    d->q0[i] = s.q0;
-    d->ql[i] = s.ql;
-    d->k0[i] = s.k0;
-    d->kl[i] = s.kl;
-    d->nsp[i] = s.nsp;
-    d->sbase[i] = d->slots;
-    d->cbase[i] = d->groups;
+    const PlanSeq& s = seq[i];
+    d->seq[i] = {s.q0, s.ql, s.k0, s.kl, s.nsp, 0, d->slots, d->groups};
     if (s.nsp > 1) {
       d->slots += s.e * kv_heads;
-      d->groups += tiles(s, d->nq) * kv_heads;
-      rows = std::max(rows, std::min(s.ql, d->P * d->nq) * d->G);
+      d->groups += tiles(s) * kv_heads;
+      d->slot_rows = std::max(d->slot_rows, std::min(s.ql, d->P * d->nq) * d->G);
     }
   }
-  d->slot_rows = rows;
   int at = 0;
   for (int i = d->n_seqs - 1; i >= 0; --i) {
-    d->ustart[i] = at;
+    d->seq[i].ustart = at;
     const int below = i + 1 < d->n_seqs ? seq[i + 1].e : 0;
     at += (seq[i].e - below) * (i + 1) * kv_heads;
   }
   d->units = at;
 }
 
+void packed_plan(const int32_t* spans, int n, int heads, int kv_heads, int num_sms, PackedPlan* tile,
+                 PackedPlan* token) {
+  memset(tile, 0, sizeof(*tile));
+  memset(token, 0, sizeof(*token));
+  tile->G = token->G = heads / kv_heads;
+  tile->P = token->P = AP_ROWS / tile->G;
+  std::vector<PlanSeq> big, few;
+  int max_ql = 0;
+  long long few_keys = 0;
+  for (int i = 0; i < n; ++i) {
+    const int32_t* t = spans + 4 * i;
+    if (t[1] == 0) continue;
+    const PlanSeq s{t[0], t[1], t[2], t[3], 0, 1};
+    if (static_cast<long long>(s.ql) * tile->G <= AT_MAX_ROWS) {
+      few.push_back(s);
+      few_keys += static_cast<long long>(s.kl) * kv_heads;
+    } else {
+      big.push_back(s);
+      max_ql = std::max(max_ql, s.ql);
+    }
+  }
+  if (!few.empty()) {
+    const long long places = 2ll * num_sms;
+    const long long range = std::min<long long>(
+        AT_MAX_KEYS, std::max<long long>(AT_MIN_KEYS, (few_keys + places - 1) / places));
+    for (PlanSeq& s : few) s.nsp = std::max(1, static_cast<int>((s.kl + range - 1) / range));
+    token->nq = 1;
+    plan_finish(few, kv_heads, token);
+  }
+  if (big.empty()) return;
+  PackedPlan* d = tile;
+  auto tiles = [&](const PlanSeq& s, int nq) { return (s.ql + d->P * nq - 1) / (d->P * nq); };
+  auto key_tiles = [&](const PlanSeq& s, int nq, int ct) {   // of query tile group ct
+    const long long end = static_cast<long long>(s.kl) - s.ql + std::min((ct + 1) * d->P * nq, s.ql);
+    return end > 0 ? (end + AP_ROWS - 1) / AP_ROWS : 0ll;
+  };
+  long long units2 = 0;
+  for (const PlanSeq& s : big) units2 += static_cast<long long>(tiles(s, 2)) * kv_heads;
+  d->nq = max_ql > d->P && units2 >= num_sms ? 2 : 1;
+  long long total = 0, longest = 0;
+  for (const PlanSeq& s : big) {
+    const int t = tiles(s, d->nq);
+    for (int c = 0; c < t; ++c) total += key_tiles(s, d->nq, c) * kv_heads;
+    longest = std::max(longest, key_tiles(s, d->nq, t - 1));
+  }
+  const long long share = (total + num_sms - 1) / num_sms;
+  const long long range = std::max<long long>(AP_MIN_RANGE, share);
+  if (longest >= 2 * range)
+    for (PlanSeq& s : big) {
+      const long long k = key_tiles(s, d->nq, tiles(s, d->nq) - 1);
+      if (k >= 2 * range) s.nsp = static_cast<int>((k + range - 1) / range);
+    }
+  plan_finish(big, kv_heads, d);
+}
+
 size_t packed_plan_bytes(const PackedPlan& d) {
-  return static_cast<size_t>(d.slots) * d.slot_rows * (128 + 2) * sizeof(float);
+  return (static_cast<size_t>(d.slots) * d.slot_rows * (128 + 2) * sizeof(float) + 15) & ~static_cast<size_t>(15);
 }
 
 // Largest dynamic shared memory of a kernel, set once per device.
@@ -634,39 +1005,67 @@ static bool allow_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
   return true;
 }
 
-int launch_attention_packed(const PackedAttnParams& a, const PackedPlan& plan, cudaStream_t st) {
-  if (plan.units == 0) return 0;
-  static std::atomic<uint64_t> done{0};
-  if (!allow_smem(ap_kernel, AP_SMEM, done)) {
-    launch_result();
-    return -1;
-  }
-  CUtensorMap tq, tk, tv;
-  if (!make_tmap_rows3(&tq, a.q, 128, a.heads, a.q_rows, static_cast<uint64_t>(a.ldq) * 2, 64, plan.G, plan.P))
-    return -2;
-  if (a.k_rows == 0) {   // no keys at all: every row is 0 and nothing is loaded
-    tk = tq;
-    tv = tq;
-  } else if (!make_tmap_2d(&tk, a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<uint64_t>(a.kv_heads) * 128,
-                    a.k_rows, static_cast<uint64_t>(a.ldk) * 2, 64, AP_ROWS) ||
-      !make_tmap_2d(&tv, a.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<uint64_t>(a.kv_heads) * 128,
-                    a.k_rows, static_cast<uint64_t>(a.ldv) * 2, 64, AP_ROWS))
-    return -2;
+static int launch_join(const ApKernelParams& p, cudaStream_t st) {
+  if (p.plan.groups == 0) return 0;
+  launch_pdl(ap_join_kernel, dim3(p.plan.groups, p.plan.slot_rows), dim3(32 * AP_JOIN_WARPS), 0, st, 1, p);
+  return launch_result();
+}
+
+int launch_attention_packed(const PackedAttnParams& a, const PackedPlan& tile, const PackedPlan& token,
+                            cudaStream_t st) {
   ApKernelParams p;
-  p.plan = plan;
+  p.q = a.q;
+  p.ldq = a.ldq;
   p.o = a.o;
   p.ldo = a.ldo;
-  p.heads = a.heads;
   p.kv_heads = a.kv_heads;
   p.sm_scale = a.sm_scale;
-  p.part_o = static_cast<float*>(a.scratch);
-  p.part_ml = a.scratch ? p.part_o + static_cast<size_t>(plan.slots) * plan.slot_rows * 128 : nullptr;
   p.status = a.status;
-  launch_pdl(ap_kernel, dim3(plan.units), dim3(AP_THREADS), AP_SMEM, st, 1, tq, tk, tv, p);
-  if (launch_result()) return -1;
-  if (plan.groups > 0) {
-    launch_pdl(ap_join_kernel, dim3(plan.groups), dim3(AP_JOIN_THREADS), 0, st, 1, p);
-    return launch_result();
+  uint8_t* scratch = static_cast<uint8_t*>(a.scratch);
+  auto partials = [&](const PackedPlan& d, size_t at) {
+    p.plan = d;
+    p.part_o = reinterpret_cast<float*>(scratch + at);
+    p.part_ml = p.part_o + static_cast<size_t>(d.slots) * d.slot_rows * 128;
+  };
+  // K and V maps; without any key row nothing is loaded and they lie over q
+  auto kv_maps = [&](CUtensorMap* tk, CUtensorMap* tv, uint32_t keys) {
+    const bool none = a.k_rows == 0;
+    const uint64_t width = static_cast<uint64_t>(a.kv_heads) * 128, n = none ? a.q_rows : a.k_rows;
+    return make_tmap_2d(tk, none ? a.q : a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, width, n,
+                        static_cast<uint64_t>(none ? a.ldq : a.ldk) * 2, 64, keys) &&
+           make_tmap_2d(tv, none ? a.q : a.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, width, n,
+                        static_cast<uint64_t>(none ? a.ldq : a.ldv) * 2, 64, keys);
+  };
+  if (tile.units > 0) {
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(ap_kernel, AP_SMEM, done)) {
+      launch_result();
+      return -1;
+    }
+    CUtensorMap tq, tk, tv;
+    if (!make_tmap_rows3(&tq, a.q, 128, a.heads, a.q_rows, static_cast<uint64_t>(a.ldq) * 2, 64, tile.G, tile.P) ||
+        !kv_maps(&tk, &tv, AP_ROWS))
+      return -2;
+    partials(tile, 0);
+    launch_pdl(ap_kernel, dim3(tile.units), dim3(AP_THREADS), AP_SMEM, st, 1, tq, tk, tv, p);
+    if (launch_result() || launch_join(p, st)) return -1;
+  }
+  if (token.units > 0) {
+    int rows = 0;
+    for (int i = 0; i < token.n_seqs; ++i) rows = std::max(rows, token.seq[i].ql * token.G);
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(ap_token_kernel, AT_SMEM, done)) {
+      launch_result();
+      return -1;
+    }
+    CUtensorMap tk, tv;
+    if (!kv_maps(&tk, &tv, AT_KEYS)) return -2;
+    partials(token, packed_plan_bytes(tile));
+    p.row_blocks = (rows + 15) / 16;
+    const long long total = static_cast<long long>(token.units) * p.row_blocks;
+    const int grid = static_cast<int>(std::min<long long>(total, 2ll * a.num_sms));
+    launch_pdl(ap_token_kernel, dim3(grid), dim3(AT_THREADS), AT_SMEM, st, 1, tk, tv, p);
+    if (launch_result() || launch_join(p, st)) return -1;
   }
   return 0;
 }

@@ -339,16 +339,17 @@ struct PackedPlan {
   int n_seqs;             // sequences with queries
   int G, P;               // query heads per key/value head; query positions per 128-row tile
   int nq;                 // 128-row query tiles per CTA (1 or 2)
-  int units;              // CTAs
+  int units;              // units of work (query tile group, key/value head, key range)
   int slots;              // partial results (0: no sequence is split over its keys)
   int slot_rows;          // rows of one partial result
-  int groups;             // CTAs of the combining kernel
-  // sequences in launch order
-  int q0[AP_MAX_SEQS], ql[AP_MAX_SEQS], k0[AP_MAX_SEQS], kl[AP_MAX_SEQS];
-  int nsp[AP_MAX_SEQS];   // key-range splits of each of the sequence's query tiles
-  int ustart[AP_MAX_SEQS];   // first CTA of the levels that sequences 0..i share
-  int sbase[AP_MAX_SEQS];    // first partial result of a split sequence
-  int cbase[AP_MAX_SEQS];    // first combining CTA of a split sequence
+  int groups;             // split (query tile group, key/value head)s
+  struct Seq {            // in launch order
+    int q0, ql, k0, kl;
+    int nsp;              // key-range splits of each of the sequence's query tiles
+    int ustart;           // first unit of the levels that sequences 0..i share
+    int sbase;            // first partial result, if split
+    int cbase;            // first group of the joining kernel, if split
+  } seq[AP_MAX_SEQS];
 };
 struct PackedAttnParams {
   const uint16_t* q;
@@ -358,11 +359,15 @@ struct PackedAttnParams {
   int ldq, ldk, ldv, ldo;
   int q_rows, k_rows, heads, kv_heads;
   float sm_scale;
-  void* scratch;          // packed_plan_bytes() of device scratch (null if 0)
+  int num_sms;
+  void* scratch;          // packed_plan_bytes() of both plans, the tile plan's first (null if 0)
   int* status;
 };
-void packed_plan(const int32_t* spans, int n, int heads, int kv_heads, int num_sms, PackedPlan* plan);
-size_t packed_plan_bytes(const PackedPlan& plan);
-int launch_attention_packed(const PackedAttnParams& p, const PackedPlan& plan, cudaStream_t st);
+// tile: sequences of many rows, token: of few (see qi_attn_packed.cu).
+void packed_plan(const int32_t* spans, int n, int heads, int kv_heads, int num_sms, PackedPlan* tile,
+                 PackedPlan* token);
+size_t packed_plan_bytes(const PackedPlan& plan);   // a multiple of 16
+int launch_attention_packed(const PackedAttnParams& p, const PackedPlan& tile, const PackedPlan& token,
+                            cudaStream_t st);
 
 }  // namespace qi

@@ -106,9 +106,9 @@ int qi_attn_causal_packed_workspace_bytes(qi_ctx* ctx, const int32_t* spans, int
   if (!ctx || !bytes) return fail(QI_ERR_INVALID_ARG, "NULL argument");
   int r;
   if ((r = check_spans(spans, n_seqs, heads, kv_heads, -1, -1))) return r;
-  qi::PackedPlan plan;
-  qi::packed_plan(spans, n_seqs, heads, kv_heads, ctx->num_sms, &plan);
-  *bytes = qi::packed_plan_bytes(plan);
+  qi::PackedPlan tile, token;
+  qi::packed_plan(spans, n_seqs, heads, kv_heads, ctx->num_sms, &tile, &token);
+  *bytes = qi::packed_plan_bytes(tile) + qi::packed_plan_bytes(token);
   return QI_OK;
 } catch (const std::bad_alloc&) {
   return fail(QI_ERR_INVALID_ARG, "out of host memory");
@@ -135,16 +135,16 @@ int qi_attn_causal_packed(qi_ctx* ctx, const uint16_t* q, int ldq, int q_rows, c
   if (overlap(o, ob, k, kb) || overlap(o, ob, v, vb) ||
       overlap(o, ob, q, span_bytes(q_rows, heads * 128, ldq)))
     return fail(QI_ERR_INVALID_ARG, "o overlaps q, k or v");
-  qi::PackedPlan plan;
-  qi::packed_plan(spans, n_seqs, heads, kv_heads, ctx->num_sms, &plan);
-  const size_t need = qi::packed_plan_bytes(plan);
+  qi::PackedPlan tile, token;
+  qi::packed_plan(spans, n_seqs, heads, kv_heads, ctx->num_sms, &tile, &token);
+  const size_t need = qi::packed_plan_bytes(tile) + qi::packed_plan_bytes(token);
   if (need > 0) {
     if (!workspace || workspace_bytes < need)
       return fail(QI_ERR_WORKSPACE, "packed attention needs %zu bytes of workspace, got %zu", need,
                   workspace ? workspace_bytes : static_cast<size_t>(0));
     if (!aligned16(workspace)) return fail(QI_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
   }
-  if (plan.units == 0) return QI_OK;
+  if (tile.units == 0 && token.units == 0) return QI_OK;
   qi::PackedAttnParams p;
   p.q = q;
   p.k = k;
@@ -159,12 +159,13 @@ int qi_attn_causal_packed(qi_ctx* ctx, const uint16_t* q, int ldq, int q_rows, c
   p.heads = heads;
   p.kv_heads = kv_heads;
   p.sm_scale = sm_scale;
+  p.num_sms = ctx->num_sms;
   p.scratch = need > 0 ? workspace : nullptr;
   p.status = ctx->status;
   DeviceScope dev(ctx);
   if (!dev.ok) return cuda_fail("cudaSetDevice");
   Prof pr(ctx, QI_KCLASS_ATTN, S(stream));
-  return check_launch(qi::launch_attention_packed(p, plan, S(stream)), "packed attention launch");
+  return check_launch(qi::launch_attention_packed(p, tile, token, S(stream)), "packed attention launch");
 } catch (const std::bad_alloc&) {
   return fail(QI_ERR_INVALID_ARG, "out of host memory");
 }
