@@ -11,22 +11,29 @@
 // Layout of the work.  The G = heads / kv_heads query heads that share a
 // key/value head are packed into the rows of one 128-row tile: row r of a
 // tile is head r mod G at query position p0 + r / G, so one 128-key tile of K
-// and V serves all of them and a short prompt or a single token (G rows)
-// still reads each key once.  A tile holds P = 128 / G positions; rows past
-// P G and past the sequence's last query are computed and dropped.  A CTA
-// takes nq = 2 neighbouring tiles A and B of a sequence, whose MMAs and
-// softmax alternate, or nq = 1 when there are too few tiles to fill the GPU.
+// and V serves all of them and a short prompt still fills its tiles.  A tile
+// holds P = 128 / G positions; rows past P G and past the sequence's last
+// query are computed and dropped.  Two CTAs share an SM.
 //
-// TMEM (512 columns): S_A | S_B | O_A | O_B.  Per key tile: S = Q K^T (both
-// operands in shared memory), one thread per row takes the softmax, writes P
-// as bf16 over S, and O += P V reads P from TMEM.  P is rounded to bf16 for
-// the tensor core; the row sum adds the unrounded fp32 values.
+// Per 128-key tile: S = Q K^T (both operands in shared memory), one thread per
+// row takes the softmax, writes P as bf16 over S, and O += P V reads P from
+// TMEM (256 columns a CTA: S | O).  P is rounded to bf16 for the tensor core;
+// the row sum adds the unrounded fp32 values.  PV(j) and S(j + 1) are issued
+// together, and one commit tells that both are complete, that the K and V
+// tiles may be replaced (one stage each: a load has the whole softmax of a
+// tile to arrive) and that S(j + 1) can be read.  What bounds a CTA is that
+// chain, softmax - PV - S - softmax; the two CTAs of an SM fill each other's
+// gaps.  A CTA runs through several query tiles: S of the next one's first
+// key tile follows the last PV of this one, so its loads and its MMA lie under
+// the last softmax and the division and store of O.
+//
+// The last key tile is cut to the keys that some row sees (in steps of 16 for the MMAs, 32 for the softmax).
 //
 // Rows that a sequence does not own: the last key tile may reach into the
 // next sequence or into rows of a cache that were never written.  Their
 // scores are masked, and their V rows, whose weight is 0 but whose values may
 // be infinite or NaN, are kept out of the product: P V runs over the 16-key
-// steps that hold a visible key, and the producer warp clears the rows between
+// steps that hold a visible key, and the softmax warps clear the rows between
 // the last visible key and the end of its step.
 //
 // Few rows (single tokens: ql G <= AT_MAX_ROWS) leave such a tile almost empty
@@ -49,12 +56,11 @@
 namespace qi {
 
 constexpr int AP_ROWS = 128;
-constexpr int AP_THREADS = 320;   // 8 softmax warps, TMA (and the V tail), MMA
-constexpr int AP_KST = 3;
-constexpr int AP_VST = 2;
+constexpr int AP_THREADS = 192;   // 4 softmax warps, TMA, MMA
 constexpr int AP_TILE = 128 * 128 * 2;
 constexpr int AP_HALF = 128 * 128;
-constexpr int AP_SMEM = 1024 + (2 + AP_KST + AP_VST) * AP_TILE + 256;
+constexpr int AP_SMEM = 1024 + 3 * AP_TILE + 128;   // Q, K, V
+static_assert(2 * (AP_SMEM + 1024) <= 233472, "two CTAs per SM");
 
 struct ApKernelParams {
   PackedPlan plan;
@@ -69,16 +75,15 @@ struct ApKernelParams {
   int* status;
 };
 
-// CTA -> (sequence, query tile group, key/value head, key split).  Sequences
-// are sorted by their number of units per head, E = tile groups x splits;
+// Unit -> (sequence, query tile, key/value head, key split).  Sequences are
+// sorted by their number of units per head, E = query tiles x splits;
 // level e takes unit e, counted from the sequence's end, of every sequence
 // that has one, so long key ranges start first and the last CTAs are short.
 struct ApUnit {
   int s, ct, h, j;
 };
 __host__ __device__ __forceinline__ int ap_tiles(const PackedPlan& d, int s) {
-  const int per = d.P * d.nq;
-  return (d.seq[s].ql + per - 1) / per;
+  return (d.seq[s].ql + d.P - 1) / d.P;
 }
 __host__ __device__ __forceinline__ ApUnit ap_unit(const PackedPlan& d, int kv_heads, int b) {
   // ustart falls with i: the levels shared by sequences 0..i begin at ustart[i]
@@ -104,8 +109,6 @@ __host__ __device__ __forceinline__ int ap_slot(const PackedPlan& d, int kv_head
   return d.seq[s].sbase + (ct * d.seq[s].nsp + j) * kv_heads + h;
 }
 
-__device__ __forceinline__ void ap_softmax_bar() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
 __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* smem, int x,
                                             int y, int z) {
   asm volatile(
@@ -123,7 +126,102 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, i
                : "memory");
 }
 
-__global__ void __launch_bounds__(AP_THREADS, 1)
+// Unit number of a CTA's round: one of every gridDim.x, alternately from the
+// front and the back of each round, so that longest-first order evens out.
+__device__ __forceinline__ int ap_unit_of(int round) {
+  const int n = static_cast<int>(gridDim.x), i = static_cast<int>(blockIdx.x);
+  return round * n + ((round & 1) ? n - 1 - i : i);
+}
+
+// tmem_ld32 without the wait, and the wait that releases its registers: every
+// use of the values comes after an asm statement that "changes" them, so none
+// can be scheduled before the data has arrived.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(taddr)
+               : "memory");
+}
+template <bool WAIT>
+__device__ __forceinline__ void tmem_ld32_ready(uint32_t (&r)[32]) {
+  if (WAIT) asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) :: "memory");
+}
+
+// One arrival for the warp, after what all its lanes did before.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// A unit of the tile kernel: a query tile over key tiles [lo, lo + n).
+struct ApWork {
+  ApUnit u;
+  int lo, n;
+  int tail;     // keys of the last of them that some row sees (128: all)
+};
+__device__ __forceinline__ ApWork ap_work(const PackedPlan& d, int kv_heads, int b) {
+  ApWork w;
+  w.u = ap_unit(d, kv_heads, b);
+  const PackedPlan::Seq& s = d.seq[w.u.s];
+  const int end = max(0, s.kl - s.ql + min((w.u.ct + 1) * d.P, s.ql));   // keys that some row sees
+  const int tiles = (end + AP_ROWS - 1) / AP_ROWS;
+  w.lo = 0;
+  int hi = tiles;
+  if (s.nsp > 1) {
+    w.lo = static_cast<int>(static_cast<long long>(tiles) * w.u.j / s.nsp);
+    hi = static_cast<int>(static_cast<long long>(tiles) * (w.u.j + 1) / s.nsp);
+  }
+  w.n = hi - w.lo;
+  w.tail = w.n > 0 && hi == tiles ? end - (tiles - 1) * AP_ROWS : AP_ROWS;
+  return w;
+}
+
+// The units of a CTA, decoded 32 at a time: lane i of a warp holds round
+// base + i, and a lookup is a shuffle (a decode is a search and several
+// divisions, too long to do between two short units).  Warp-collective.
+struct ApList {
+  int base, at, ct, lo, n, j;   // at: sequence, head; lo: with the tail
+  __device__ __forceinline__ void fill(const PackedPlan& d, int kv_heads, int from) {
+    base = from;
+    const int b = ap_unit_of(from + (threadIdx.x & 31));
+    n = -1;   // past the last unit
+    if (b < d.units) {
+      const ApWork w = ap_work(d, kv_heads, b);
+      at = w.u.s | (w.u.h << 8);             // s < 256
+      ct = w.u.ct;
+      lo = w.lo | ((w.tail - 1) << 24);      // tiles below 2^24, tail 1..128
+      n = w.n;
+      j = w.u.j;
+    }
+    __syncwarp();
+  }
+  // n < 0: there is no such round
+  __device__ __forceinline__ ApWork get(const PackedPlan& d, int kv_heads, int round) {
+    if (round - base >= 32) fill(d, kv_heads, round);
+    const int i = round - base;
+    ApWork w;
+    const int a = __shfl_sync(0xffffffffu, at, i), l = __shfl_sync(0xffffffffu, lo, i);
+    w.u.ct = __shfl_sync(0xffffffffu, ct, i);
+    w.n = __shfl_sync(0xffffffffu, n, i);
+    w.u.j = __shfl_sync(0xffffffffu, j, i);
+    w.u.s = a & 255;
+    w.u.h = a >> 8;
+    w.lo = l & 0xFFFFFF;
+    w.tail = (l >> 24) + 1;
+    return w;
+  }
+  // the next unit with key tiles, from `round` on
+  __device__ __forceinline__ ApWork next(const PackedPlan& d, int kv_heads, int& round) {
+    ApWork w;
+    do w = get(d, kv_heads, round++);
+    while (w.n == 0);
+    return w;
+  }
+};
+static_assert(AP_MAX_SEQS <= 256, "sequence in 8 bits");
+
+__global__ void __launch_bounds__(AP_THREADS, 2)
     ap_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ ApKernelParams p) {
   const PackedPlan& d = p.plan;
@@ -131,375 +229,346 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
   extern __shared__ uint8_t ap_smem_raw[];
   const uint32_t raw_addr = smem_u32(ap_smem_raw);
   uint8_t* smem = ap_smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  uint8_t* sQ = smem;                              // [2][AP_TILE]
-  uint8_t* sK = smem + 2 * AP_TILE;                // [AP_KST][AP_TILE]
-  uint8_t* sV = smem + (2 + AP_KST) * AP_TILE;     // [AP_VST][AP_TILE]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (2 + AP_KST + AP_VST) * AP_TILE);
-  uint64_t* q_full = bars + 0;
-  uint64_t* k_full = bars + 1;                     // [AP_KST]
-  uint64_t* k_empty = k_full + AP_KST;             // [AP_KST]
-  uint64_t* v_full = k_empty + AP_KST;             // [AP_VST]
-  uint64_t* v_empty = v_full + AP_VST;             // [AP_VST]
-  uint64_t* s_full = v_empty + AP_VST;             // [2] per query tile
-  uint64_t* p_full = s_full + 2;                   // [2]
-  uint64_t* o_full = p_full + 2;
-  uint64_t* drain = o_full + 1;
-  uint64_t* v_landed = drain + 1;                  // the last V tile is in shared memory ...
-  uint64_t* v_tail = v_landed + 1;                 // ... and its rows past the keys are cleared
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_tail + 1);
-  uint8_t* stage = smem;   // output rows, over Q (free once every MMA has completed)
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + AP_TILE;
+  uint8_t* sV = smem + 2 * AP_TILE;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + 3 * AP_TILE);
+  uint64_t* k_full = q_full + 1;
+  uint64_t* v_full = q_full + 2;
+  uint64_t* s_full = q_full + 3;   // S of a tile and P V of the tile before complete
+  uint64_t* p_full = q_full + 4;
+  uint64_t* o_full = q_full + 5;   // the last P V of a unit complete
+  uint64_t* drain = q_full + 6;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 7);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const ApUnit u = ap_unit(d, p.kv_heads, static_cast<int>(blockIdx.x));
-  const int G = d.G, P = d.P, nq = d.nq;
-  const int ql = d.seq[u.s].ql, kl = d.seq[u.s].kl, k0s = d.seq[u.s].k0, nsp = d.seq[u.s].nsp;
-  const int p0 = u.ct * P * nq;                    // first query position of this CTA
-  const int first = kl - ql + 1;                   // keys that query position 0 sees (may be negative)
-  // keys that the last position of tile X sees, and its key tiles
-  int n_all[2];
-#pragma unroll
-  for (int X = 0; X < 2; ++X) {
-    const int last = min(p0 + (X + 1) * P, ql) - 1;   // < p0 + X P: the tile has no query
-    const int end = X < nq && last >= p0 + X * P ? max(0, first + last) : 0;
-    n_all[X] = (end + AP_ROWS - 1) / AP_ROWS;
-  }
-  const int kv_end = max(0, first + min(p0 + nq * P, ql) - 1);   // keys that some row of this CTA sees
-  const int n_tot = max(n_all[0], n_all[1]);
-  const int lo = static_cast<int>(static_cast<long long>(n_tot) * u.j / nsp);
-  const int hi = static_cast<int>(static_cast<long long>(n_tot) * (u.j + 1) / nsp);
-  // this CTA's key tiles are [lo, hi); local tile i drives the rings and phases
-  const int n_x0 = max(0, min(n_all[0], hi) - lo), n_x1 = max(0, min(n_all[1], hi) - lo);
-  const int n_kv = hi - lo;
-  // keys of the last tile some row sees; < 128: rows behind them must not reach P V
-  const int tail = hi == n_tot && n_kv > 0 ? kv_end - (n_tot - 1) * AP_ROWS : AP_ROWS;
-
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    for (int s = 0; s < AP_KST; ++s) {
-      mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
-    }
-    for (int s = 0; s < AP_VST; ++s) {
-      mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 1);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 128);
-    }
+    mbar_init(k_full, 1);
+    mbar_init(v_full, 1);
+    mbar_init(s_full, 1);
+    mbar_init(p_full, 4);
     mbar_init(o_full, 1);
     mbar_init(drain, 1);
-    mbar_init(v_landed, 1);
-    mbar_init(v_tail, 1);
     fence_mbar_init();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == 4 && lane == 0) {
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
-  if (warp == 9) {
-    tmem_alloc(tmem_slot, 512);
+  if (warp == 5) {
+    tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
   }
+  const int G = d.G, P = d.P;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // every role walks the same list of units, decoded from the launch's arguments alone
+  ApList list;
+  list.fill(d, p.kv_heads, 0);
   pdl_wait();
   pdl_trigger();
 
-  if (warp == 8) {
+  if (warp == 4) {
     // ------------------------------------------------------------ TMA producer
     bool ok = true;
-    if (lane == 0 && n_kv > 0) {
+    int round = 0, t = 0, units = 0;   // t: key tiles of the units before this one
+    ApWork w = list.next(d, p.kv_heads, round);
+    auto load_q = [&](const ApWork& x) {
       // a box holds P positions x G heads x 64 head columns: rows in tile order
-      const uint32_t q_bytes = static_cast<uint32_t>(P * G) * 128 * 2;
-      mbar_arrive_expect_tx(q_full, nq * q_bytes);
-      for (int t = 0; t < nq; ++t)
-        for (int half = 0; half < 2; ++half)
-          tma_load_3d(&tmQ, q_full, sQ + t * AP_TILE + half * AP_HALF, 64 * half, u.h * G,
-                      d.seq[u.s].q0 + p0 + t * P);
-      int jk = 0, jv = 0;   // tiles whose loads were issued
-      for (int j = 0; j < n_kv; ++j) {
-        const int row = k0s + (lo + j) * AP_ROWS;
-        const int ks = j % AP_KST, kr = j / AP_KST;
-        if (!mbar_wait(&k_empty[ks], (kr & 1) ^ 1u, status)) { ok = false; break; }
-        mbar_arrive_expect_tx(&k_full[ks], AP_TILE);
-        for (int half = 0; half < 2; ++half)
-          tma_load_2d(&tmK, &k_full[ks], sK + ks * AP_TILE + half * AP_HALF, u.h * 128 + 64 * half, row);
-        jk = j + 1;
-        const int vs = j % AP_VST, vr = j / AP_VST;
-        if (!mbar_wait(&v_empty[vs], (vr & 1) ^ 1u, status)) { ok = false; break; }
-        mbar_arrive_expect_tx(&v_full[vs], AP_TILE);
-        for (int half = 0; half < 2; ++half)
-          tma_load_2d(&tmV, &v_full[vs], sV + vs * AP_TILE + half * AP_HALF, u.h * 128 + 64 * half, row);
-        jv = j + 1;
+      mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(P * G) * 128 * 2);
+      for (int half = 0; half < 2; ++half)
+        tma_load_3d(&tmQ, q_full, sQ + half * AP_HALF, 64 * half, x.u.h * G, d.seq[x.u.s].q0 + x.u.ct * P);
+      ++units;
+    };
+    auto load = [&](const CUtensorMap* map, uint64_t* bar, uint8_t* dst, const ApWork& x, int j) {
+      mbar_arrive_expect_tx(bar, AP_TILE);
+      for (int half = 0; half < 2; ++half)
+        tma_load_2d(map, bar, dst + half * AP_HALF, x.u.h * 128 + 64 * half, d.seq[x.u.s].k0 + (x.lo + j) * AP_ROWS);
+    };
+    int nk = 0, nv = 0;   // K and V tiles asked for
+    if (lane == 0 && w.n >= 0) {
+      load_q(w);
+      load(&tmK, k_full, sK, w, 0);
+      load(&tmV, v_full, sV, w, 0);
+      nk = nv = 1;
+    }
+    while (w.n >= 0) {
+      const ApWork nx = list.next(d, p.kv_heads, round);
+      if (lane == 0) {
+        for (int j = 0; j < w.n; ++j) {
+          if (j + 1 == w.n && nx.n < 0 && nv == t + w.n) break;   // everything is on its way
+          // S of tile t + j and P V of the one before complete: Q (after a unit's last S), K of
+          // this tile and V of the one before have been used
+          if (!mbar_wait(s_full, (t + j) & 1, status)) { ok = false; break; }
+          if (t + j > 0) { load(&tmV, v_full, sV, w, j); ++nv; }
+          if (j + 1 < w.n) {
+            load(&tmK, k_full, sK, w, j + 1);
+            ++nk;
+          } else if (nx.n >= 0) {
+            load_q(nx);
+            load(&tmK, k_full, sK, nx, 0);
+            ++nk;
+          }
+        }
       }
-      if (!ok) {
-        // bounded drain of the loads already armed (Q, the last K and V tiles)
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      t += w.n;
+      w = nx;
+    }
+    if (!ok && lane == 0) {   // bounded drain of the loads already armed
+      uint64_t* bars[3] = {q_full, k_full, v_full};
+      const int count[3] = {units, nk, nv};
+      for (int i = 0; i < 3; ++i) {
         const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(q_full, 0) && globaltimer_ns() - t0 < QI_WAIT_NS) {
-        }
-        for (int jj = (jk > AP_KST ? jk - AP_KST : 0); jj < jk; ++jj) {
-          const uint64_t t1 = globaltimer_ns();
-          while (!mbar_try_wait(&k_full[jj % AP_KST], (jj / AP_KST) & 1) &&
-                 globaltimer_ns() - t1 < QI_WAIT_NS) {
-          }
-        }
-        for (int jj = (jv > AP_VST ? jv - AP_VST : 0); jj < jv; ++jj) {
-          const uint64_t t1 = globaltimer_ns();
-          while (!mbar_try_wait(&v_full[jj % AP_VST], (jj / AP_VST) & 1) &&
-                 globaltimer_ns() - t1 < QI_WAIT_NS) {
-          }
+        while (count[i] > 0 && !mbar_try_wait(bars[i], (count[i] - 1) & 1) && globaltimer_ns() - t0 < QI_WAIT_NS) {
         }
       }
     }
-    // V tail: clear the last tile's rows from the last visible key to the end
-    // of its 16-key step (the swizzle permutes inside a 128-byte row)
-    if (__all_sync(0xffffffffu, ok) && tail < AP_ROWS && n_kv > 0) {
-      const int st = (n_kv - 1) % AP_VST;
-      if (mbar_wait_warp(v_landed, 0, status) &&
-          mbar_wait_warp(&v_full[st], ((n_kv - 1) / AP_VST) & 1, status)) {
-        const int rows = ((tail + 15) & ~15) - tail;
-        for (int i = lane; i < rows * 16; i += 32)
-          *reinterpret_cast<uint4*>(sV + st * AP_TILE + ((i >> 3) & 1) * AP_HALF + (tail + (i >> 4)) * 128 +
-                                    (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_tail);
-      }
-    }
-  } else if (warp == 9) {
+  } else if (warp == 5) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && n_kv > 0) {
-      constexpr uint32_t idesc_s = umma_idesc(false, 128, 128);
-      constexpr uint32_t idesc_pv = umma_idesc(false, 128, 128) | (1u << 16);   // B MN-major
-      bool ok = mbar_wait(q_full, 0, status);
-      bool landed = false;
-      auto issue_s = [&](int X, int jj) -> bool {
-        const int st = jj % AP_KST;
-        if (!mbar_wait(&k_full[st], (jj / AP_KST) & 1, status)) return false;
-        tc_fence_after();
-        const uint32_t qa = smem_u32(sQ + X * AP_TILE), kb = smem_u32(sK + st * AP_TILE);
+    constexpr uint32_t idesc_m = umma_idesc(false, 128, 0);
+    constexpr uint32_t idesc_pv = umma_idesc(false, 128, 128) | (1u << 16);   // B MN-major
+    const uint64_t qd = umma_desc_kmajor_sw128(smem_u32(sQ)), kd = umma_desc_kmajor_sw128(smem_u32(sK));
+    const uint64_t vd = umma_desc_mnmajor_sw128(smem_u32(sV), AP_HALF);
+    bool ok = true;
+    int round = 0, t = 0, units = 0;
+    auto issue_s = [&](const ApWork& x, int j, int ti) -> bool {
+      if ((j == 0 && !mbar_wait(q_full, units & 1, status)) || !mbar_wait(k_full, ti & 1, status)) return false;
+      if (j == 0) ++units;
+      tc_fence_after();
+      const uint32_t cols = j == x.n - 1 ? static_cast<uint32_t>(x.tail + 15) / 16 * 16 : 128u;
+      const uint32_t idesc = idesc_m | ((cols >> 3) << 17);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (kk >> 2) * AP_HALF + (kk & 3) * 32;
-          umma_f16(tmem_base + X * 128, umma_desc_kmajor_sw128(qa + off),
-                   umma_desc_kmajor_sw128(kb + off), idesc_s, kk > 0);
-        }
-        umma_commit(&s_full[X]);
-        return true;
-      };
-      auto issue_pv = [&](int X, int jj) -> bool {
-        const int st = jj % AP_VST;
-        const bool cut = jj == n_kv - 1 && tail < AP_ROWS;
-        if (!mbar_wait(&v_full[st], (jj / AP_VST) & 1, status)) return false;
-        if (cut && !landed) {   // cleared while the softmax runs
-          mbar_arrive(v_landed);
-          landed = true;
-        }
-        if (!mbar_wait(&p_full[X], jj & 1, status)) return false;
-        if (cut && !mbar_wait(v_tail, 0, status)) return false;
-        tc_fence_after();
-        const uint32_t vb = smem_u32(sV + st * AP_TILE);
-        const int steps = cut ? (tail + 15) / 16 : 8;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)   // 16 keys per instruction
-          if (kk < steps)
-            umma_f16_ts(tmem_base + 256 + X * 128, tmem_base + X * 128 + kk * 8,
-                        umma_desc_mnmajor_sw128(vb + kk * 2048, AP_HALF), idesc_pv,
-                        (jj > 0 || kk > 0) ? 1u : 0u);
-        return true;
-      };
-      if (ok) {
-        if (n_x0 > 0) ok = issue_s(0, 0);
-        if (ok && n_x1 > 0) ok = issue_s(1, 0);
-        if (ok) umma_commit(&k_empty[0]);
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint64_t off = static_cast<uint64_t>((kk >> 2) * AP_HALF + (kk & 3) * 32) >> 4;
+        umma_f16(tmem_base, qd + off, kd + off, idesc, kk > 0);
       }
-      for (int j = 0; ok && j < n_kv; ++j) {
-        if (j < n_x0) ok = issue_pv(0, j);
-        if (ok && j + 1 < n_x0) ok = issue_s(0, j + 1);
-        if (ok && j < n_x1) ok = issue_pv(1, j);
-        if (ok) umma_commit(&v_empty[j % AP_VST]);
-        if (ok && j + 1 < n_kv) {
-          if (j + 1 < n_x1) ok = issue_s(1, j + 1);
-          if (ok) umma_commit(&k_empty[(j + 1) % AP_KST]);
+      umma_commit(s_full);
+      return true;
+    };
+    ApWork w = list.next(d, p.kv_heads, round);
+    if (lane == 0 && w.n >= 0) ok = issue_s(w, 0, 0);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    while (ok && w.n >= 0) {
+      const ApWork nx = list.next(d, p.kv_heads, round);
+      if (lane == 0) {
+        for (int j = 0; ok && j < w.n; ++j) {
+          ok = mbar_wait(v_full, (t + j) & 1, status) && mbar_wait(p_full, (t + j) & 1, status);
+          if (!ok) break;
+          tc_fence_after();
+          const int steps = j == w.n - 1 ? (w.tail + 15) / 16 : 8;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)   // 16 keys per instruction
+            if (kk < steps)
+              umma_f16_ts(tmem_base + 128, tmem_base + 64 + kk * 8, vd + static_cast<uint64_t>(kk * 2048 >> 4), idesc_pv,
+                          (j > 0 || kk > 0) ? 1u : 0u);
+          if (j + 1 < w.n) {
+            ok = issue_s(w, j + 1, t + j + 1);
+          } else {
+            umma_commit(o_full);
+            if (nx.n >= 0) ok = issue_s(nx, 0, t + w.n);
+          }
         }
       }
-      if (ok) {
-        umma_commit(o_full);
-      } else {
-        umma_commit(drain);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < QI_WAIT_NS) {
-        }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      t += w.n;
+      w = nx;
+    }
+    if (!ok && lane == 0) {   // no MMA may still run when TMEM is released
+      umma_commit(drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < QI_WAIT_NS) {
       }
     }
   } else {
     // ------------------------------------------------------------ softmax + epilogue
-    const int X = warp >> 2;
-    const int quarter = warp & 3;
-    const int row = quarter * 32 + lane;
-    const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t tS = tmem_base + lane_bits + X * 128;
-    const uint32_t tO = tmem_base + lane_bits + 256 + X * 128;
-    const int n_mine = X == 0 ? n_x0 : n_x1;
-    const int pos = p0 + X * P + row / G;           // query position of this row
-    const bool live = X < nq && row < P * G && pos < ql;
-    const int lim = live ? max(0, first + pos) : 0;   // keys this row sees
-    // keys that every live row of this warp sees: tiles below need no mask
-    const int lim_min = __reduce_min_sync(0xffffffffu, live ? lim : 0x7fffffff);
+    const int row = warp * 32 + lane;
+    const uint32_t lane_bits = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t tS = tmem_base + lane_bits, tO = tmem_base + lane_bits + 128;
+    const int row_pos = row / G, row_head = row - row_pos * G;
     const float sl2 = p.sm_scale * 1.4426950408889634f;
-    float m_ref = 0.f;   // reference maximum, base-2 scaled
-    float l = 0.f;
-    bool seen = false;   // m_ref holds a score
-    const bool warp_live = __any_sync(0xffffffffu, live);
     bool ok = true;
-    for (int j = 0; j < n_mine; ++j) {
-      if (!mbar_wait_warp(&s_full[X], j & 1, status)) { ok = false; break; }
-      tc_fence_after();
-      if (!warp_live) {   // no query in these 32 rows: whatever O gets is dropped
-        mbar_arrive(&p_full[X]);
-        continue;
-      }
-      const int k0 = (lo + j) * AP_ROWS;
-      uint32_t r[128];
-      tmem_ld128(tS, r);
-      if (k0 + AP_ROWS > lim_min) {
+    int t = 0, units = 0;   // tiles of the units before this one, units with key tiles
+    for (int round = 0; ok; ++round) {
+      const ApWork w = list.get(d, p.kv_heads, round);
+      if (w.n < 0) break;
+      const PackedPlan::Seq& sq = d.seq[w.u.s];
+      const int pos = w.u.ct * P + row_pos;           // query position of this row
+      const bool live = row < P * G && pos < sq.ql;
+      const int lim = live ? max(0, sq.kl - sq.ql + 1 + pos) : 0;   // keys this row sees
+      // keys that every live row of this warp sees: tiles below need no mask
+      const int lim_min = __reduce_min_sync(0xffffffffu, live ? lim : 0x7fffffff);
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      float m_ref = -INFINITY;   // reference maximum, base-2 scaled; -inf: no score yet
+      float l = 0.f;
+      for (int j = 0; j < w.n; ++j) {
+        if (!mbar_wait_warp(s_full, (t + j) & 1, status)) { ok = false; break; }
+        tc_fence_after();
+        const int k0 = (w.lo + j) * AP_ROWS;
+        const int ncols = j == w.n - 1 ? w.tail : AP_ROWS;   // the same for every row
+        if (warp_live) {   // (otherwise: no query in these 32 rows, and whatever O gets is dropped)
+          // The row's maximum over columns 0-63, then 64-127; the exponentials over 64-127, which are
+          // still in registers, then over 0-63, read again: 64 scores are held at a time.  (A whole
+          // row does not fit beside the rest, and what spills goes to L2: shared memory leaves little
+          // L1.)  P goes over columns 64-127 of S.  Columns past the cut are masked.
+          uint32_t r[2][32];
+          auto start = [&](int h) {
+            tmem_ld32_start(tS + 64 * h, r[0]);
+            tmem_ld32_start(tS + 64 * h + 32, r[1]);
+          };
+          auto finish = [&](int h) {
+            tmem_ld32_ready<true>(r[0]);
+            tmem_ld32_ready<false>(r[1]);
+            if (k0 + 64 * h + 64 > lim_min) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i)
-          if (k0 + i >= lim) r[i] = __float_as_uint(-INFINITY);
-      }
-      float m8[8];
+              for (int i = 0; i < 64; ++i)
+                if (k0 + 64 * h + i >= lim) r[i >> 5][i & 31] = __float_as_uint(-INFINITY);
+            }
+          };
+          auto maximum = [&]() {
+            float m8[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) m8[k] = fmaxf(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+            for (int k = 0; k < 8; ++k) m8[k] = fmaxf(__uint_as_float(r[0][2 * k]), __uint_as_float(r[0][2 * k + 1]));
 #pragma unroll
-      for (int i = 16; i < 128; i += 16)
+            for (int i = 16; i < 64; i += 16)
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          m8[k] = fmax3(m8[k], __uint_as_float(r[i + 2 * k]), __uint_as_float(r[i + 2 * k + 1]));
-      const float mx2 = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * sl2;
-      if (!seen && mx2 > -INFINITY) {   // the row's first score: P was 0 until now
-        seen = true;
-        m_ref = mx2;
-      }
-      const bool grow = mx2 > m_ref + 8.0f;
-      if (__any_sync(0xffffffffu, grow)) {
-        float f = 1.0f;
-        if (grow) {
-          f = exp2f(m_ref - mx2);
-          l *= f;
-          m_ref = mx2;
+              for (int k = 0; k < 8; ++k)
+                m8[k] = fmax3(m8[k], __uint_as_float(r[i >> 5][(i & 31) + 2 * k]),
+                              __uint_as_float(r[i >> 5][(i & 31) + 2 * k + 1]));
+            return fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+          };
+          start(0);
+          finish(0);
+          float mx2 = maximum();
+          if (ncols > 64) {
+            start(1);
+            finish(1);
+            mx2 = fmaxf(mx2, maximum());
+          }
+          mx2 *= sl2;
+          // the reference moves only when the maximum exceeds it by more than 8 (P <= 256)
+          const float old = m_ref;
+          if (mx2 > old + 8.0f || old == -INFINITY) m_ref = mx2;
+          const bool grow = m_ref != old && old != -INFINITY;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float f = grow ? exp2f(old - m_ref) : 1.0f;
+            l *= f;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {   // (P V of the tile before is complete: S came after it)
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32(tO + c * 32, o);
+            }
+            tmem_st_wait();
+          }
+          const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+          const uint64_t sl2x2 = f2_pack(sl2, sl2);
+          const uint64_t negm2 = f2_pack(neg, neg);
+          uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+          auto weights = [&](int h) {
+#pragma unroll
+            for (int c = 1; c >= 0; --c) {
+              if (64 * h + 32 * c >= ncols) continue;   // P V does not read further
+              uint32_t pk[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float s0 = __uint_as_float(r[c][2 * i]), s1 = __uint_as_float(r[c][2 * i + 1]);
+                const uint64_t x2 = f2_fma(f2_pack(s0, s1), sl2x2, negm2);
+                float x0, x1;
+                f2_unpack(x2, x0, x1);
+                const float e0 = ex2_approx(x0);
+                const float e1 = ex2_approx(x1);
+                acc2[i & 3] = f2_add(acc2[i & 3], f2_pack(e0, e1));
+                pk[i] = pack_bf16x2(e0, e1);
+              }
+              tmem_st16(tS + 64 + h * 32 + c * 16, pk);
+            }
+          };
+          if (ncols > 64) {
+            weights(1);
+            start(0);
+            finish(0);
+          }
+          weights(0);
+          float a0, a1, b0, b1;
+          f2_unpack(f2_add(acc2[0], acc2[1]), a0, a1);
+          f2_unpack(f2_add(acc2[2], acc2[3]), b0, b1);
+          l += (a0 + b0) + (a1 + b1);
+          tmem_st_wait();
         }
+        if (ncols & 15) {
+          // clear V from the last visible key to the end of its 16-key step (the swizzle permutes
+          // inside a 128-byte row); S of this tile being complete, the V tile before has been used
+          if (!mbar_wait_warp(v_full, (t + j) & 1, status)) { ok = false; break; }
+          const int n_clear = ((ncols + 15) & ~15) - ncols;
+          for (int i = row; i < n_clear * 16; i += 128)
+            *reinterpret_cast<uint4*>(sV + ((i >> 3) & 1) * AP_HALF + (ncols + (i >> 4)) * 128 + (i & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        warp_arrive(p_full, lane);
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      // where this row goes: fp32 partial of the key range, or the output (a thread writes its own
+      // row: staging rows through shared memory for wider segments takes several times the
+      // load/store instructions, which queue behind the other CTA's exponentials)
+      const bool split = sq.nsp > 1;
+      const size_t at = split ? static_cast<size_t>(ap_slot(d, p.kv_heads, w.u.s, w.u.ct, w.u.h, w.u.j)) *
+                                        d.slot_rows + row
+                              : static_cast<size_t>(sq.q0 + pos) * p.ldo + (w.u.h * G + row_head) * 128;
+      const float inv = l > 0.f ? __fdividef(1.0f, l) : 0.f;
+      const uint64_t inv2 = f2_pack(inv, inv);
+      if (w.n > 0 && !mbar_wait_warp(o_full, units & 1, status)) { ok = false; break; }
+      tc_fence_after();
+      if (split && live) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m_ref, l);
+      if (warp_live && (w.n > 0 || !split)) {   // (a range without a key has weight 0, whatever its O)
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + c * 32, o);
+          uint32_t r[32];
+          if (w.n > 0) tmem_ld32(tO + 32 * c, r);
+          if (!live) continue;
+          if (split) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + at * 128 + c * 32);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st32(tO + c * 32, o);
-        }
-        tmem_st_wait();
-      }
-      const uint64_t sl2x2 = f2_pack(sl2, sl2);
-      const uint64_t negm2 = f2_pack(-m_ref, -m_ref);
-      uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+            for (int v = 0; v < 8; ++v)
+              dst[v] = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
+                                   __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(p.o + at + c * 32);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
+            for (int v = 0; v < 4; ++v) {
+              uint32_t y[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float s0 = __uint_as_float(r[32 * c + 2 * i]), s1 = __uint_as_float(r[32 * c + 2 * i + 1]);
-          const uint64_t x2 = f2_fma(f2_pack(s0, s1), sl2x2, negm2);
-          float x0, x1;
-          f2_unpack(x2, x0, x1);
-          const float e0 = ex2_approx(x0);
-          const float e1 = ex2_approx(x1);
-          acc2[i & 3] = f2_add(acc2[i & 3], f2_pack(e0, e1));
-          pk[i] = pack_bf16x2(e0, e1);
-        }
-        tmem_st16(tS + c * 16, pk);
-      }
-      float a0, a1, b0, b1;
-      f2_unpack(f2_add(acc2[0], acc2[1]), a0, a1);
-      f2_unpack(f2_add(acc2[2], acc2[3]), b0, b1);
-      l += (a0 + b0) + (a1 + b1);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&p_full[X]);
-    }
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok && n_kv > 0) ok = mbar_wait_warp(o_full, 0, status);
-    tc_fence_after();
-    const bool have = n_mine > 0;   // O of this tile was written
-    if (X < nq && ok && nsp > 1) {
-      // partial result of this key range (rows packed from the CTA's first)
-      const int prow = X * P * G + row;
-      const size_t at = static_cast<size_t>(ap_slot(d, p.kv_heads, u.s, u.ct, u.h, u.j)) * d.slot_rows + prow;
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-        if (have) tmem_ld32(tO + c * 32, r);
-        if (live && have) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + at * 128 + c * 32);
-#pragma unroll
-          for (int v = 0; v < 8; ++v)
-            dst[v] = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
-                                 __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
-        }
-      }
-      if (live) {
-        p.part_ml[2 * at] = m_ref;
-        p.part_ml[2 * at + 1] = have ? l : 0.f;   // 0: this range has no weight
-      }
-    } else if (X < nq && ok) {
-      const float inv = l > 0.f ? 1.0f / l : 0.f;
-      const uint64_t inv2 = f2_pack(inv, inv);
-      uint8_t* rows = stage + X * AP_TILE + quarter * 32 * 256;   // this warp's 32 rows of 256 bytes
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-        if (have) {
-          tmem_ld32(tO + c * 32, r);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = 0u;
-        }
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float a, b;
-            f2_unpack(f2_mul(f2_pack(__uint_as_float(r[8 * v + 2 * e]), __uint_as_float(r[8 * v + 2 * e + 1])), inv2), a, b);
-            w[e] = lim == 0 ? 0u : pack_bf16x2(a, b);   // a row that sees no key: 0
+              for (int e = 0; e < 4; ++e) {
+                float a, b;
+                f2_unpack(f2_mul(f2_pack(__uint_as_float(r[8 * v + 2 * e]), __uint_as_float(r[8 * v + 2 * e + 1])), inv2), a, b);
+                y[e] = lim == 0 ? 0u : pack_bf16x2(a, b);   // a row that sees no key: 0
+              }
+              dst[v] = make_uint4(y[0], y[1], y[2], y[3]);
+            }
           }
-          // 16-byte chunk x of row i at chunk x ^ (i mod 16): no bank conflicts either way
-          *reinterpret_cast<uint4*>(rows + lane * 256 + (((c * 4 + v) ^ (lane & 15)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      __syncwarp();
-      // each half warp copies one row: 256 contiguous bytes of the output
-#pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        const int rr = 2 * i + (lane >> 4), x = lane & 15;
-        const int tr = quarter * 32 + rr, ps = p0 + X * P + tr / G;
-        if (tr < P * G && ps < ql) {
-          const uint4 w = *reinterpret_cast<const uint4*>(rows + rr * 256 + ((x ^ (rr & 15)) << 4));
-          *reinterpret_cast<uint4*>(p.o + static_cast<size_t>(d.seq[u.s].q0 + ps) * p.ldo +
-                                    (u.h * G + tr % G) * 128 + x * 8) = w;
-        }
-      }
+      t += w.n;
+      if (w.n > 0) ++units;
+      tc_fence_before();   // O has been read before the next unit's P lets P V write it
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 5) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, 512);
+    tmem_dealloc(tmem_base, 256);
   }
 }
 
@@ -577,12 +646,6 @@ __global__ void __launch_bounds__(AT_THREADS, 2)
   }
   __syncthreads();
 
-  // The units of this CTA: one of every gridDim.x, alternately from the front
-  // and the back of each round, so that longest-first order evens out.
-  auto unit_of = [&](int round) {
-    const int n = static_cast<int>(gridDim.x), i = static_cast<int>(blockIdx.x);
-    return round * n + ((round & 1) ? n - 1 - i : i);
-  };
   struct Work {
     ApUnit u;
     int r0, rows, lo, hi;   // first of 16 rows, rows of the unit, 64-key steps
@@ -603,8 +666,8 @@ __global__ void __launch_bounds__(AT_THREADS, 2)
     if (lane == 0) {
       prefetch_tmap(&tmK);
       prefetch_tmap(&tmV);
-      if (unit_of(0) < total) {
-        const Work w = work_of(unit_of(0));
+      if (ap_unit_of(0) < total) {
+        const Work w = work_of(ap_unit_of(0));
         for (int st = w.lo; st < w.hi; ++st)
           for (int half = 0; half < 2; ++half) {
             tma_prefetch_2d(&tmK, w.u.h * 128 + 64 * half, d.seq[w.u.s].k0 + st * AT_KEYS);
@@ -617,8 +680,8 @@ __global__ void __launch_bounds__(AT_THREADS, 2)
     if (lane == 0) {
       bool ok = true;
       int i = 0;   // steps loaded, over all units
-      for (int round = 0; ok && unit_of(round) < total; ++round) {
-        const Work w = work_of(unit_of(round));
+      for (int round = 0; ok && ap_unit_of(round) < total; ++round) {
+        const Work w = work_of(ap_unit_of(round));
         for (int st = w.lo; st < w.hi; ++st, ++i) {
           const int sl = i % AT_STAGES;
           if (!mbar_wait(&empty[sl], ((i / AT_STAGES) & 1) ^ 1u, status)) { ok = false; break; }
@@ -643,7 +706,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2)
   }
 
   // -------------------------------------------------------------- compute warps
-  Work w = work_of(min(unit_of(0), total - 1));
+  Work w = work_of(min(ap_unit_of(0), total - 1));
   pdl_wait();
   pdl_trigger();
   const float sl2 = p.sm_scale * 1.4426950408889634f;
@@ -652,8 +715,8 @@ __global__ void __launch_bounds__(AT_THREADS, 2)
   // V: matrices (keys 0-7, 8-15) x (two 8-column groups)
   const int mrow = warp * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, mcol = lane >> 4;
   int i = 0;   // steps taken, over all units
-  for (int round = 0; unit_of(round) < total; ++round) {
-    if (round > 0) w = work_of(unit_of(round));
+  for (int round = 0; ap_unit_of(round) < total; ++round) {
+    if (round > 0) w = work_of(ap_unit_of(round));
     const PackedPlan::Seq& sq = d.seq[w.u.s];
     const int ql = sq.ql, kl = sq.kl, nsp = sq.nsp, r0 = w.r0, rows = w.rows;
     if (r0 >= rows) continue;
@@ -841,8 +904,8 @@ __global__ void __launch_bounds__(32 * AP_JOIN_WARPS) ap_join_kernel(const __gri
     else s_hi = mid - 1;
   }
   const int ct = (b - d.seq[s].cbase) / p.kv_heads, h = (b - d.seq[s].cbase) % p.kv_heads;
-  const int G = d.G, nsp = d.seq[s].nsp, p0 = ct * d.P * d.nq;
-  const int n_rows = min(d.P * d.nq, d.seq[s].ql - p0) * G;
+  const int G = d.G, nsp = d.seq[s].nsp, p0 = ct * d.P;
+  const int n_rows = min(d.P, d.seq[s].ql - p0) * G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t step = static_cast<size_t>(p.kv_heads) * d.slot_rows;
   const size_t at = static_cast<size_t>(ap_slot(d, p.kv_heads, s, ct, h, 0)) * d.slot_rows + r;
@@ -892,12 +955,10 @@ __global__ void __launch_bounds__(32 * AP_JOIN_WARPS) ap_join_kernel(const __gri
 // Launch plans of a table of sequences, one for the tile kernel and one for the
 // token kernel: a pure function of the arguments.
 //  * sequences of at most AT_MAX_ROWS rows go to the token kernel.
-//  * tile kernel: nq = 2 (two query tiles share a CTA's key stream and hide each
-//    other's softmax) unless that leaves SMs without a CTA or every sequence
-//    has no more positions than one tile holds; key ranges are split when the
-//    longest CTA would outlast the average load of an SM, into ranges of about
-//    that average, at least AP_MIN_RANGE key tiles (a range costs a partial
-//    result and the joining kernel).
+//  * tile kernel: key ranges are split when the longest unit would outlast the
+//    average load of an SM, into ranges of about that average, at least
+//    AP_MIN_RANGE key tiles (a range costs a partial result and the joining
+//    kernel).
 //  * token kernel: two CTAs fit on an SM; ranges are as long as gives every
 //    place one CTA, but between AT_MIN_KEYS (fewer keys do not pay for a
 //    partial result) and AT_MAX_KEYS (shorter CTAs even out ragged lengths).
@@ -908,10 +969,10 @@ struct PlanSeq {
   int q0, ql, k0, kl, e, nsp;
 };
 
-// Launch order, partial results and CTA numbers of a plan whose nq and splits are chosen.
+// Launch order, partial results and CTA numbers of a plan whose splits are chosen.
 static void plan_finish(std::vector<PlanSeq>& seq, int kv_heads, PackedPlan* d) {
   d->n_seqs = static_cast<int>(seq.size());
-  auto tiles = [&](const PlanSeq& s) { return (s.ql + d->P * d->nq - 1) / (d->P * d->nq); };
+  auto tiles = [&](const PlanSeq& s) { return (s.ql + d->P - 1) / d->P; };
   for (PlanSeq& s : seq) s.e = tiles(s) * s.nsp;
   std::stable_sort(seq.begin(), seq.end(), [](const PlanSeq& a, const PlanSeq& b) {
     return a.e != b.e ? a.e > b.e : a.kl > b.kl;
@@ -922,7 +983,7 @@ static void plan_finish(std::vector<PlanSeq>& seq, int kv_heads, PackedPlan* d) 
     if (s.nsp > 1) {
       d->slots += s.e * kv_heads;
       d->groups += tiles(s) * kv_heads;
-      d->slot_rows = std::max(d->slot_rows, std::min(s.ql, d->P * d->nq) * d->G);
+      d->slot_rows = std::max(d->slot_rows, std::min(s.ql, d->P) * d->G);
     }
   }
   int at = 0;
@@ -941,7 +1002,6 @@ void packed_plan(const int32_t* spans, int n, int heads, int kv_heads, int num_s
   tile->G = token->G = heads / kv_heads;
   tile->P = token->P = AP_ROWS / tile->G;
   std::vector<PlanSeq> big, few;
-  int max_ql = 0;
   long long few_keys = 0;
   for (int i = 0; i < n; ++i) {
     const int32_t* t = spans + 4 * i;
@@ -952,7 +1012,6 @@ void packed_plan(const int32_t* spans, int n, int heads, int kv_heads, int num_s
       few_keys += static_cast<long long>(s.kl) * kv_heads;
     } else {
       big.push_back(s);
-      max_ql = std::max(max_ql, s.ql);
     }
   }
   if (!few.empty()) {
@@ -960,30 +1019,26 @@ void packed_plan(const int32_t* spans, int n, int heads, int kv_heads, int num_s
     const long long range = std::min<long long>(
         AT_MAX_KEYS, std::max<long long>(AT_MIN_KEYS, (few_keys + places - 1) / places));
     for (PlanSeq& s : few) s.nsp = std::max(1, static_cast<int>((s.kl + range - 1) / range));
-    token->nq = 1;
     plan_finish(few, kv_heads, token);
   }
   if (big.empty()) return;
   PackedPlan* d = tile;
-  auto tiles = [&](const PlanSeq& s, int nq) { return (s.ql + d->P * nq - 1) / (d->P * nq); };
-  auto key_tiles = [&](const PlanSeq& s, int nq, int ct) {   // of query tile group ct
-    const long long end = static_cast<long long>(s.kl) - s.ql + std::min((ct + 1) * d->P * nq, s.ql);
+  auto tiles = [&](const PlanSeq& s) { return (s.ql + d->P - 1) / d->P; };
+  auto key_tiles = [&](const PlanSeq& s, int ct) {   // of query tile ct
+    const long long end = static_cast<long long>(s.kl) - s.ql + std::min((ct + 1) * d->P, s.ql);
     return end > 0 ? (end + AP_ROWS - 1) / AP_ROWS : 0ll;
   };
-  long long units2 = 0;
-  for (const PlanSeq& s : big) units2 += static_cast<long long>(tiles(s, 2)) * kv_heads;
-  d->nq = max_ql > d->P && units2 >= num_sms ? 2 : 1;
   long long total = 0, longest = 0;
   for (const PlanSeq& s : big) {
-    const int t = tiles(s, d->nq);
-    for (int c = 0; c < t; ++c) total += key_tiles(s, d->nq, c) * kv_heads;
-    longest = std::max(longest, key_tiles(s, d->nq, t - 1));
+    const int t = tiles(s);
+    for (int c = 0; c < t; ++c) total += key_tiles(s, c) * kv_heads;
+    longest = std::max(longest, key_tiles(s, t - 1));
   }
   const long long share = (total + num_sms - 1) / num_sms;
   const long long range = std::max<long long>(AP_MIN_RANGE, share);
   if (longest >= 2 * range)
     for (PlanSeq& s : big) {
-      const long long k = key_tiles(s, d->nq, tiles(s, d->nq) - 1);
+      const long long k = key_tiles(s, tiles(s) - 1);
       if (k >= 2 * range) s.nsp = static_cast<int>((k + range - 1) / range);
     }
   plan_finish(big, kv_heads, d);
@@ -1047,7 +1102,7 @@ int launch_attention_packed(const PackedAttnParams& a, const PackedPlan& tile, c
         !kv_maps(&tk, &tv, AP_ROWS))
       return -2;
     partials(tile, 0);
-    launch_pdl(ap_kernel, dim3(tile.units), dim3(AP_THREADS), AP_SMEM, st, 1, tq, tk, tv, p);
+    launch_pdl(ap_kernel, dim3(std::min(tile.units, 2 * a.num_sms)), dim3(AP_THREADS), AP_SMEM, st, 1, tq, tk, tv, p);
     if (launch_result() || launch_join(p, st)) return -1;
   }
   if (token.units > 0) {

@@ -338,11 +338,10 @@ constexpr int AP_MAX_SEQS = 256;
 struct PackedPlan {
   int n_seqs;             // sequences with queries
   int G, P;               // query heads per key/value head; query positions per 128-row tile
-  int nq;                 // 128-row query tiles per CTA (1 or 2)
-  int units;              // units of work (query tile group, key/value head, key range)
+  int units;              // units of work (query tile, key/value head, key range)
   int slots;              // partial results (0: no sequence is split over its keys)
   int slot_rows;          // rows of one partial result
-  int groups;             // split (query tile group, key/value head)s
+  int groups;             // split (query tile, key/value head)s
   struct Seq {            // in launch order
     int q0, ql, k0, kl;
     int nsp;              // key-range splits of each of the sequence's query tiles

@@ -507,15 +507,18 @@ def _rows(ctx: Context, t: Optional[torch.Tensor], name: str, cols: int):
     with unit column stride."""
     if t is None:
         return None, 0
-    if not t.is_cuda or t.device.index != ctx.device or t.dtype != torch.bfloat16 or t.dim() != 2:
+    if t.dtype is not torch.bfloat16 or t.get_device() != ctx.device or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D bf16 tensor on cuda:{ctx.device}")
-    if t.shape[1] != cols:
-        raise ValueError(f"{name} has {t.shape[1]} columns, expected {cols}")
+    rows, width = t.shape
+    if width != cols:
+        raise ValueError(f"{name} has {width} columns, expected {cols}")
+    if rows <= 1 or t.is_contiguous():      # (one row: the distance between rows means nothing)
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have unit column stride")
+        return t.data_ptr(), cols
     ld, step = t.stride()
     if cols > 1 and step != 1:
         raise ValueError(f"{name} must have unit column stride")
-    if t.shape[0] <= 1:      # the distance between rows means nothing
-        return t.data_ptr(), cols
     if ld < cols:
         raise ValueError(f"{name} has overlapping rows")
     return t.data_ptr(), ld
@@ -524,14 +527,16 @@ def _rows(ctx: Context, t: Optional[torch.Tensor], name: str, cols: int):
 def _new(shape, like: torch.Tensor, stream, dtype=torch.bfloat16):
     """An output or workspace tensor, allocated on the stream that will write it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _on(ctx: Context, stream) -> int:
     """Stream handle of a call: `stream`, or the current one of the context's device."""
-    return (stream if stream is not None else torch.cuda.current_stream(ctx.device)).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(ctx.device)   # current_stream() without the object
 
 
 def qi_attn_causal_packed_workspace_bytes(ctx: Context, spans: torch.Tensor, heads: int,
