@@ -344,8 +344,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   pdl_trigger();
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    // ------------------------------------------------------------ producer (the whole warp, one lane issues)
+    {
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -353,41 +353,35 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         int pr, mt, nt;
         mm_tile<PAIR, BN, EPI>(p, tile, pr, mt, nt);
         const int m0 = mt * (PAIR ? 256 : 128) + rank * 128;
-        const int total_kb = p.num_kb[pr] * p.segs;
-        for (int kb = 0; kb < total_kb; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, p.status)) { ok = false; break; }
-          const int seg = kb >= p.num_kb[pr] ? 1 : 0;   // segs == 2 only for a single product
-          const int k = (kb - seg * p.num_kb[pr]) * 64;
-          const int ia = pr + seg;
-          uint8_t* da = sA + stage * C::A_BYTES;
-          uint8_t* db = sB + stage * C::B_BYTES;
-          const uint32_t fb = PAIR ? mapa_shared(smem_u32(&full[stage]), 0) : 0u;
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * C::STAGE_BYTES);
-          auto load = [&](const CUtensorMap* map, uint8_t* dst, int x, int y) {
-            if (PAIR) tma_load_2d_pair(map, fb, dst, x, y);
-            else tma_load_2d(map, &full[stage], dst, x, y);
-          };
-          if (AMN) {
+        const int num_kb = p.num_kb[pr];
+        for (int seg = 0; seg < p.segs && ok; ++seg) {   // segs == 2 only for a single product
+          const CUtensorMap* ma = &maps.a[pr + seg];
+          const CUtensorMap* mb = &maps.b[EPI == MM_GATE ? rank : pr + seg];
+          for (int kb = 0; kb < num_kb; ++kb) {
+            if (!mbar_wait_warp(&empty[stage], phase ^ 1u, p.status)) { ok = false; break; }
+            const int k = kb * 64;
+            uint8_t* da = sA + stage * C::A_BYTES;
+            uint8_t* db = sB + stage * C::B_BYTES;
+            const uint32_t fb = PAIR ? mapa_shared(smem_u32(&full[stage]), 0) : smem_u32(&full[stage]);
+            if (rank == 0) mbar_expect_elect(&full[stage], (PAIR ? 2 : 1) * C::STAGE_BYTES);
+            if (AMN) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) load(&maps.a[ia], da + i * 8192, m0 + 64 * i, k);
-          } else {
-            load(&maps.a[ia], da, k, m0);
-          }
-          if (EPI == MM_GATE) {
-            if (PAIR) {
-              load(&maps.b[rank], db, k, nt * W);
+              for (int i = 0; i < 2; ++i) tma_load_2d_elect<PAIR>(ma, fb, da + i * 8192, m0 + 64 * i, k);
             } else {
-              load(&maps.b[0], db, k, nt * W);
-              load(&maps.b[1], db + C::B_BYTES / 2, k, nt * W);
+              tma_load_2d_elect<PAIR>(ma, fb, da, k, m0);
             }
-          } else if (BMN) {
+            if (EPI == MM_GATE) {
+              tma_load_2d_elect<PAIR>(mb, fb, db, k, nt * W);
+              if (!PAIR) tma_load_2d_elect<PAIR>(&maps.b[1], fb, db + C::B_BYTES / 2, k, nt * W);
+            } else if (BMN) {
 #pragma unroll
-            for (int i = 0; i < C::B_ROWS / 64; ++i)
-              load(&maps.b[ia], db + i * 8192, nt * BN + rank * C::B_ROWS + 64 * i, k);
-          } else {
-            load(&maps.b[ia], db, k, nt * BN + rank * C::B_ROWS);
+              for (int i = 0; i < C::B_ROWS / 64; ++i)
+                tma_load_2d_elect<PAIR>(mb, fb, db + i * 8192, nt * BN + rank * C::B_ROWS + 64 * i, k);
+            } else {
+              tma_load_2d_elect<PAIR>(mb, fb, db, k, nt * BN + rank * C::B_ROWS);
+            }
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           }
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
       if (!ok) {
@@ -410,9 +404,14 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (pair: even CTA)
-    if (lane == 0 && rank == 0) {
+    // The whole warp runs the loop and one elected lane issues: operands that
+    // are uniform over a converged warp reach the tensor core's instruction
+    // without a move per lane (an MMA issued under a lane test took 54 clocks).
+    if (rank == 0) {
       constexpr uint32_t idesc = umma_idesc(false, PAIR ? 256 : 128, BN) | (AMN ? (1u << 15) : 0u) |
                                  (BMN ? (1u << 16) : 0u);
+      const uint64_t adesc0 = AMN ? umma_desc_mnmajor_sw128(smem_u32(sA), 8192) : umma_desc_kmajor_sw128(smem_u32(sA));
+      const uint64_t bdesc0 = BMN ? umma_desc_mnmajor_sw128(smem_u32(sB), 8192) : umma_desc_kmajor_sw128(smem_u32(sB));
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -422,37 +421,34 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         int pr, mt, nt;
         mm_tile<PAIR, BN, EPI>(p, tile, pr, mt, nt);
         const int total_kb = p.num_kb[pr] * p.segs;
-        if (!(PAIR ? mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, p.status)
-                   : mbar_wait(&tempty[acc], acc_phase ^ 1u, p.status))) { ok = false; break; }
+        const bool free = PAIR ? mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, p.status)
+                               : mbar_wait(&tempty[acc], acc_phase ^ 1u, p.status);
+        if (!__all_sync(0xffffffffu, free)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
         for (int kb = 0; kb < total_kb; ++kb) {
-          if (!mbar_wait(&full[stage], phase, p.status)) { ok = false; break; }
+          if (!mbar_wait_warp(&full[stage], phase, p.status)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t aa = smem_u32(sA + stage * C::A_BYTES), ba = smem_u32(sB + stage * C::B_BYTES);
-          const uint64_t adesc = AMN ? umma_desc_mnmajor_sw128(aa, 8192) : umma_desc_kmajor_sw128(aa);
-          const uint64_t bdesc = BMN ? umma_desc_mnmajor_sw128(ba, 8192) : umma_desc_kmajor_sw128(ba);
+          const uint64_t adesc = adesc0 + static_cast<uint64_t>(stage * (C::A_BYTES >> 4));
+          const uint64_t bdesc = bdesc0 + static_cast<uint64_t>(stage * (C::B_BYTES >> 4));
 #pragma unroll
           for (int k = 0; k < 4; ++k) {   // 16 values of K per instruction: 32 bytes of a K-major row, 16 MN-major rows
             const uint64_t ao = static_cast<uint64_t>(k * (AMN ? 2048 : 32)) >> 4;
             const uint64_t bo = static_cast<uint64_t>(k * (BMN ? 2048 : 32)) >> 4;
-            if (PAIR) umma_f16_pair(d_tmem, adesc + ao, bdesc + bo, idesc, (kb | k) != 0);
-            else umma_f16(d_tmem, adesc + ao, bdesc + bo, idesc, (kb | k) != 0);
+            umma_f16_elect<PAIR>(d_tmem, adesc + ao, bdesc + bo, idesc, (kb | k) != 0);
           }
-          if (PAIR) umma_commit_pair(&empty[stage], 0x3);
-          else umma_commit(&empty[stage]);
+          umma_commit_elect<PAIR>(&empty[stage]);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        if (PAIR) umma_commit_pair(&tfull[acc], 0x3);
-        else umma_commit(&tfull[acc]);
+        umma_commit_elect<PAIR>(&tfull[acc]);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
       if (!ok) {
         // make sure no MMA is still writing TMEM before it is released
-        if (PAIR) umma_commit_pair(drain, 0x1);
-        else umma_commit(drain);
+        if (PAIR) umma_commit_elect<true>(drain, 0x1);
+        else umma_commit_elect<false>(drain);
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < QI_WAIT_NS) {
         }
