@@ -109,12 +109,15 @@ __host__ __device__ __forceinline__ int ap_slot(const PackedPlan& d, int kv_head
   return d.seq[s].sbase + (ct * d.seq[s].nsp + j) * kv_heads + h;
 }
 
-__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* smem, int x,
-                                            int y, int z) {
+// tma_load_2d_elect with three coordinates.
+__device__ __forceinline__ void tma_load_3d_elect(const CUtensorMap* map, uint32_t bar, void* smem, int x, int y,
+                                                  int z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(smem_u32(smem)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
 
@@ -146,6 +149,16 @@ template <bool WAIT>
 __device__ __forceinline__ void tmem_ld32_ready(uint32_t (&r)[32]) {
   if (WAIT) asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
   asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) :: "memory");
+}
+
+// 16 columns, loaded and waited for in one statement.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 
 // One arrival for the warp, after what all its lanes did before.
@@ -273,54 +286,52 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   pdl_trigger();
 
   if (warp == 4) {
-    // ------------------------------------------------------------ TMA producer
+    // ------------------------------------------------------------ TMA producer (the whole warp, one lane issues)
     bool ok = true;
     int round = 0, t = 0, units = 0;   // t: key tiles of the units before this one
+    const uint32_t q_bar = smem_u32(q_full), k_bar = smem_u32(k_full), v_bar = smem_u32(v_full);
     ApWork w = list.next(d, p.kv_heads, round);
     auto load_q = [&](const ApWork& x) {
       // a box holds P positions x G heads x 64 head columns: rows in tile order
-      mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(P * G) * 128 * 2);
+      mbar_expect_elect(q_full, static_cast<uint32_t>(P * G) * 128 * 2);
       for (int half = 0; half < 2; ++half)
-        tma_load_3d(&tmQ, q_full, sQ + half * AP_HALF, 64 * half, x.u.h * G, d.seq[x.u.s].q0 + x.u.ct * P);
+        tma_load_3d_elect(&tmQ, q_bar, sQ + half * AP_HALF, 64 * half, x.u.h * G, d.seq[x.u.s].q0 + x.u.ct * P);
       ++units;
     };
-    auto load = [&](const CUtensorMap* map, uint64_t* bar, uint8_t* dst, const ApWork& x, int j) {
-      mbar_arrive_expect_tx(bar, AP_TILE);
+    auto load = [&](const CUtensorMap* map, uint64_t* full, uint32_t bar, uint8_t* dst, const ApWork& x, int j) {
+      mbar_expect_elect(full, AP_TILE);
       for (int half = 0; half < 2; ++half)
-        tma_load_2d(map, bar, dst + half * AP_HALF, x.u.h * 128 + 64 * half, d.seq[x.u.s].k0 + (x.lo + j) * AP_ROWS);
+        tma_load_2d_elect<false>(map, bar, dst + half * AP_HALF, x.u.h * 128 + 64 * half,
+                                 d.seq[x.u.s].k0 + (x.lo + j) * AP_ROWS);
     };
     int nk = 0, nv = 0;   // K and V tiles asked for
-    if (lane == 0 && w.n >= 0) {
+    if (w.n >= 0) {
       load_q(w);
-      load(&tmK, k_full, sK, w, 0);
-      load(&tmV, v_full, sV, w, 0);
+      load(&tmK, k_full, k_bar, sK, w, 0);
+      load(&tmV, v_full, v_bar, sV, w, 0);
       nk = nv = 1;
     }
-    while (w.n >= 0) {
+    while (ok && w.n >= 0) {
       const ApWork nx = list.next(d, p.kv_heads, round);
-      if (lane == 0) {
-        for (int j = 0; j < w.n; ++j) {
-          if (j + 1 == w.n && nx.n < 0 && nv == t + w.n) break;   // everything is on its way
-          // S of tile t + j and P V of the one before complete: Q (after a unit's last S), K of
-          // this tile and V of the one before have been used
-          if (!mbar_wait(s_full, (t + j) & 1, status)) { ok = false; break; }
-          if (t + j > 0) { load(&tmV, v_full, sV, w, j); ++nv; }
-          if (j + 1 < w.n) {
-            load(&tmK, k_full, sK, w, j + 1);
-            ++nk;
-          } else if (nx.n >= 0) {
-            load_q(nx);
-            load(&tmK, k_full, sK, nx, 0);
-            ++nk;
-          }
+      for (int j = 0; j < w.n; ++j) {
+        if (j + 1 == w.n && nx.n < 0 && nv == t + w.n) break;   // everything is on its way
+        // S of tile t + j and P V of the one before complete: Q (after a unit's last S), K of
+        // this tile and V of the one before have been used
+        if (!mbar_wait_warp(s_full, (t + j) & 1, status)) { ok = false; break; }
+        if (t + j > 0) { load(&tmV, v_full, v_bar, sV, w, j); ++nv; }
+        if (j + 1 < w.n) {
+          load(&tmK, k_full, k_bar, sK, w, j + 1);
+          ++nk;
+        } else if (nx.n >= 0) {
+          load_q(nx);
+          load(&tmK, k_full, k_bar, sK, nx, 0);
+          ++nk;
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
       t += w.n;
       w = nx;
     }
-    if (!ok && lane == 0) {   // bounded drain of the loads already armed
+    if (!ok) {   // bounded drain of the loads already armed
       uint64_t* bars[3] = {q_full, k_full, v_full};
       const int count[3] = {units, nk, nv};
       for (int i = 0; i < 3; ++i) {
@@ -330,7 +341,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       }
     }
   } else if (warp == 5) {
-    // ------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------ MMA issuer (the whole warp, one lane issues)
     constexpr uint32_t idesc_m = umma_idesc(false, 128, 0);
     constexpr uint32_t idesc_pv = umma_idesc(false, 128, 128) | (1u << 16);   // B MN-major
     const uint64_t qd = umma_desc_kmajor_sw128(smem_u32(sQ)), kd = umma_desc_kmajor_sw128(smem_u32(sK));
@@ -338,7 +349,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     bool ok = true;
     int round = 0, t = 0, units = 0;
     auto issue_s = [&](const ApWork& x, int j, int ti) -> bool {
-      if ((j == 0 && !mbar_wait(q_full, units & 1, status)) || !mbar_wait(k_full, ti & 1, status)) return false;
+      if ((j == 0 && !mbar_wait_warp(q_full, units & 1, status)) || !mbar_wait_warp(k_full, ti & 1, status)) return false;
       if (j == 0) ++units;
       tc_fence_after();
       const uint32_t cols = j == x.n - 1 ? static_cast<uint32_t>(x.tail + 15) / 16 * 16 : 128u;
@@ -346,41 +357,37 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
         const uint64_t off = static_cast<uint64_t>((kk >> 2) * AP_HALF + (kk & 3) * 32) >> 4;
-        umma_f16(tmem_base, qd + off, kd + off, idesc, kk > 0);
+        umma_f16_elect<false>(tmem_base, qd + off, kd + off, idesc, kk > 0);
       }
-      umma_commit(s_full);
+      umma_commit_elect<false>(s_full);
       return true;
     };
     ApWork w = list.next(d, p.kv_heads, round);
-    if (lane == 0 && w.n >= 0) ok = issue_s(w, 0, 0);
-    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (w.n >= 0) ok = issue_s(w, 0, 0);
     while (ok && w.n >= 0) {
       const ApWork nx = list.next(d, p.kv_heads, round);
-      if (lane == 0) {
-        for (int j = 0; ok && j < w.n; ++j) {
-          ok = mbar_wait(v_full, (t + j) & 1, status) && mbar_wait(p_full, (t + j) & 1, status);
-          if (!ok) break;
-          tc_fence_after();
-          const int steps = j == w.n - 1 ? (w.tail + 15) / 16 : 8;
+      for (int j = 0; ok && j < w.n; ++j) {
+        ok = mbar_wait_warp(v_full, (t + j) & 1, status) && mbar_wait_warp(p_full, (t + j) & 1, status);
+        if (!ok) break;
+        tc_fence_after();
+        const int steps = j == w.n - 1 ? (w.tail + 15) / 16 : 8;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)   // 16 keys per instruction
-            if (kk < steps)
-              umma_f16_ts(tmem_base + 128, tmem_base + 64 + kk * 8, vd + static_cast<uint64_t>(kk * 2048 >> 4), idesc_pv,
-                          (j > 0 || kk > 0) ? 1u : 0u);
-          if (j + 1 < w.n) {
-            ok = issue_s(w, j + 1, t + j + 1);
-          } else {
-            umma_commit(o_full);
-            if (nx.n >= 0) ok = issue_s(nx, 0, t + w.n);
-          }
+        for (int kk = 0; kk < 8; ++kk)   // 16 keys per instruction
+          if (kk < steps)
+            umma_f16_ts_elect(tmem_base + 128, tmem_base + 64 + kk * 8, vd + static_cast<uint64_t>(kk * 2048 >> 4),
+                              idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+        if (j + 1 < w.n) {
+          ok = issue_s(w, j + 1, t + j + 1);
+        } else {
+          umma_commit_elect<false>(o_full);
+          if (nx.n >= 0) ok = issue_s(nx, 0, t + w.n);
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       t += w.n;
       w = nx;
     }
-    if (!ok && lane == 0) {   // no MMA may still run when TMEM is released
-      umma_commit(drain);
+    if (!ok) {   // no MMA may still run when TMEM is released
+      umma_commit_elect<false>(drain);
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < QI_WAIT_NS) {
       }
@@ -459,12 +466,12 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
             const float f = grow ? exp2f(old - m_ref) : 1.0f;
             l *= f;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {   // (P V of the tile before is complete: S came after it)
-              uint32_t o[32];
-              tmem_ld32(tO + c * 32, o);
+            for (int c = 0; c < 8; ++c) {   // (P V of the tile before is complete: S came after it)
+              uint32_t o[16];
+              tmem_ld16(tO + c * 16, o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(tO + c * 32, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16(tO + c * 16, o);
             }
             tmem_st_wait();
           }
@@ -476,19 +483,22 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
 #pragma unroll
             for (int c = 1; c >= 0; --c) {
               if (64 * h + 32 * c >= ncols) continue;   // P V does not read further
-              uint32_t pk[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float s0 = __uint_as_float(r[c][2 * i]), s1 = __uint_as_float(r[c][2 * i + 1]);
-                const uint64_t x2 = f2_fma(f2_pack(s0, s1), sl2x2, negm2);
-                float x0, x1;
-                f2_unpack(x2, x0, x1);
-                const float e0 = ex2_approx(x0);
-                const float e1 = ex2_approx(x1);
-                acc2[i & 3] = f2_add(acc2[i & 3], f2_pack(e0, e1));
-                pk[i] = pack_bf16x2(e0, e1);
+              for (int q = 0; q < 2; ++q) {
+                uint32_t pk[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float s0 = __uint_as_float(r[c][16 * q + 2 * i]), s1 = __uint_as_float(r[c][16 * q + 2 * i + 1]);
+                  const uint64_t x2 = f2_fma(f2_pack(s0, s1), sl2x2, negm2);
+                  float x0, x1;
+                  f2_unpack(x2, x0, x1);
+                  const float e0 = ex2_approx(x0);
+                  const float e1 = ex2_approx(x1);
+                  acc2[i & 3] = f2_add(acc2[i & 3], f2_pack(e0, e1));
+                  pk[i] = pack_bf16x2(e0, e1);
+                }
+                tmem_st8(tS + 64 + h * 32 + c * 16 + q * 8, pk);
               }
-              tmem_st16(tS + 64 + h * 32 + c * 16, pk);
             }
           };
           if (ncols > 64) {
@@ -518,17 +528,17 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
+      if (w.n > 0 && !mbar_wait_warp(o_full, units & 1, status)) { ok = false; break; }
+      tc_fence_after();
       // where this row goes: fp32 partial of the key range, or the output (a thread writes its own
       // row: staging rows through shared memory for wider segments takes several times the
       // load/store instructions, which queue behind the other CTA's exponentials)
       const bool split = sq.nsp > 1;
+      const float inv = l > 0.f ? __fdividef(1.0f, l) : 0.f;
+      const uint64_t inv2 = f2_pack(inv, inv);
       const size_t at = split ? static_cast<size_t>(ap_slot(d, p.kv_heads, w.u.s, w.u.ct, w.u.h, w.u.j)) *
                                         d.slot_rows + row
                               : static_cast<size_t>(sq.q0 + pos) * p.ldo + (w.u.h * G + row_head) * 128;
-      const float inv = l > 0.f ? __fdividef(1.0f, l) : 0.f;
-      const uint64_t inv2 = f2_pack(inv, inv);
-      if (w.n > 0 && !mbar_wait_warp(o_full, units & 1, status)) { ok = false; break; }
-      tc_fence_after();
       if (split && live) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m_ref, l);
       if (warp_live && (w.n > 0 || !split)) {   // (a range without a key has weight 0, whatever its O)
 #pragma unroll 1
