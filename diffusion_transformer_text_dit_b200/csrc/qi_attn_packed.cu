@@ -86,6 +86,15 @@ __host__ __device__ __forceinline__ int ap_tiles(const PackedPlan& d, int s) {
   return (d.seq[s].ql + d.P - 1) / d.P;
 }
 __host__ __device__ __forceinline__ ApUnit ap_unit(const PackedPlan& d, int kv_heads, int b) {
+  if (d.n_order > 0) {
+    const int i = b / kv_heads;
+    ApUnit u;
+    u.s = static_cast<int>(d.order[i] >> 24);
+    u.ct = static_cast<int>(d.order[i] & 0xFFFFFFu);
+    u.h = b - i * kv_heads;
+    u.j = 0;
+    return u;
+  }
   // ustart falls with i: the levels shared by sequences 0..i begin at ustart[i]
   int lo = 0, hi = d.n_seqs - 1;
   while (lo < hi) {   // the first i whose levels begin at or before b
@@ -964,7 +973,9 @@ __global__ void __launch_bounds__(32 * AP_JOIN_WARPS) ap_join_kernel(const __gri
 
 // Launch plans of a table of sequences, one for the tile kernel and one for the
 // token kernel: a pure function of the arguments.
-//  * sequences of at most AT_MAX_ROWS rows go to the token kernel.
+//  * sequences of at most AT_MAX_ROWS rows go to the token kernel, except short
+//    ones beside sequences that need the tile kernel anyway: a unit more there
+//    costs less than a second kernel (about 12 us).
 //  * tile kernel: key ranges are split when the longest unit would outlast the
 //    average load of an SM, into ranges of about that average, at least
 //    AP_MIN_RANGE key tiles (a range costs a partial result and the joining
@@ -973,7 +984,7 @@ __global__ void __launch_bounds__(32 * AP_JOIN_WARPS) ap_join_kernel(const __gri
 //    place one CTA, but between AT_MIN_KEYS (fewer keys do not pay for a
 //    partial result) and AT_MAX_KEYS (shorter CTAs even out ragged lengths).
 constexpr int AP_MIN_RANGE = 4;
-constexpr int AT_MIN_KEYS = 256, AT_MAX_KEYS = 512;
+constexpr int AT_MIN_KEYS = 256, AT_MAX_KEYS = 512, AT_JOIN_KEYS = 2048;
 
 struct PlanSeq {
   int q0, ql, k0, kl, e, nsp;
@@ -1013,11 +1024,13 @@ void packed_plan(const int32_t* spans, int n, int heads, int kv_heads, int num_s
   tile->P = token->P = AP_ROWS / tile->G;
   std::vector<PlanSeq> big, few;
   long long few_keys = 0;
+  bool any_big = false;
+  for (int i = 0; i < n; ++i) any_big = any_big || static_cast<long long>(spans[4 * i + 1]) * tile->G > AT_MAX_ROWS;
   for (int i = 0; i < n; ++i) {
     const int32_t* t = spans + 4 * i;
     if (t[1] == 0) continue;
     const PlanSeq s{t[0], t[1], t[2], t[3], 0, 1};
-    if (static_cast<long long>(s.ql) * tile->G <= AT_MAX_ROWS) {
+    if (static_cast<long long>(s.ql) * tile->G <= AT_MAX_ROWS && !(any_big && s.kl <= AT_JOIN_KEYS)) {
       few.push_back(s);
       few_keys += static_cast<long long>(s.kl) * kv_heads;
     } else {
@@ -1052,6 +1065,21 @@ void packed_plan(const int32_t* spans, int n, int heads, int kv_heads, int num_s
       if (k >= 2 * range) s.nsp = static_cast<int>((k + range - 1) / range);
     }
   plan_finish(big, kv_heads, d);
+  // Exact order, longest unit first, where the table holds it and no unit is split (a counting
+  // sort over the key tiles of a unit).
+  if (d->slots > 0 || d->units > AP_MAX_ORDER * kv_heads || longest > AP_MAX_ORDER) return;
+  std::vector<int> at(static_cast<size_t>(longest) + 2, 0);
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int i = 0; i < d->n_seqs; ++i)
+      for (int c = tiles(big[i]) - 1; c >= 0; --c) {
+        const size_t cost = static_cast<size_t>(longest - key_tiles(big[i], c));   // 0: the longest
+        if (pass == 0) ++at[cost + 1];
+        else d->order[at[cost]++] = static_cast<uint32_t>(i) << 24 | static_cast<uint32_t>(c);
+      }
+    if (pass == 0)
+      for (size_t i = 1; i < at.size(); ++i) at[i] += at[i - 1];
+  }
+  d->n_order = d->units / kv_heads;
 }
 
 size_t packed_plan_bytes(const PackedPlan& d) {

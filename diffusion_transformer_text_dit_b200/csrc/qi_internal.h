@@ -335,6 +335,7 @@ int launch_gated_dw(const GatedBackwardParams& p, cudaStream_t st);        // th
 
 // Causal attention over packed sequences with grouped heads (qi_attn_causal_packed).
 constexpr int AP_MAX_SEQS = 256;
+constexpr int AP_MAX_ORDER = 1024;
 struct PackedPlan {
   int n_seqs;             // sequences with queries
   int G, P;               // query heads per key/value head; query positions per 128-row tile
@@ -349,6 +350,10 @@ struct PackedPlan {
     int sbase;            // first partial result, if split
     int cbase;            // first group of the joining kernel, if split
   } seq[AP_MAX_SEQS];
+  // units of one key/value head in launch order (sequence << 24 | query tile), if none is split
+  // and there are few enough; else n_order is 0 and the order follows from ustart
+  int n_order;
+  uint32_t order[AP_MAX_ORDER];
 };
 struct PackedAttnParams {
   const uint16_t* q;

@@ -14,15 +14,15 @@
 // transposed copy: TMA brings 64 x 64 boxes with the 128-byte swizzle and the
 // instruction descriptor's major bit says how the tensor core walks them.
 //
-// Warp roles in a 320-thread CTA (one per SM, persistent over tiles): warp 0
-// TMA producer, warp 1 TMEM allocator and MMA issuer, warps 2..9 epilogue
-// (warp w reads TMEM lanes 32 (w % 4) .. + 31; two warps share a lane quarter
-// and alternate 32-column chunks).  The accumulator is double-buffered in
-// TMEM, so the epilogue of a tile overlaps the MMAs of the next.  With PAIR
-// two CTAs share a 256 x BN tile (cta_group::2): each loads 128 rows of A and
-// half the rows of B.  MM_GATE takes half of the B rows from each weight, so
-// a tile holds BN / 2 gate columns next to the same up columns and the
-// product never leaves the registers; in a pair, each CTA loads one weight.
+// Warp roles in a 320-thread CTA: warp 0 TMA producer, warp 1 TMEM allocator
+// and MMA issuer, warps 2..9 epilogue (warp w reads TMEM lanes 32 (w % 4) .. +
+// 31; two warps share a lane quarter).  Large products run on persistent CTA
+// pairs with 256 x 256 tiles (mm_kernel), middle ones on 128 x 128 tiles whose
+// K a cluster shares (mm_split_kernel), up to 16 rows of A on warp-level MMAs
+// that stream the weights (skinny_kernel).  MM_GATE takes half of the B rows
+// from each weight, so a tile holds gate columns next to the same up columns
+// and their product never leaves the registers; in a pair, each CTA loads one
+// weight.
 #include <string.h>
 
 #include <atomic>
@@ -64,18 +64,12 @@ struct MmParams {
   int* status;
 };
 
-template <bool PAIR, int BN>
-struct MmCfg {
-  static constexpr int A_BYTES = 128 * 128;
-  static constexpr int B_ROWS = PAIR ? BN / 2 : BN;
-  static constexpr int B_BYTES = B_ROWS * 128;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN == 32 ? 10 : (BN == 64 ? 8 : 6);
-  static constexpr int TMEM_COLS = 2 * BN;
-  static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 256;
-  static_assert(2 * STAGES + 6 <= 32, "barrier area");
-  static_assert(SMEM <= 232448, "shared memory per CTA");
-};
+constexpr int MM_TILE = 128 * 128;   // bytes of a stage's A or B tile of one CTA: 128 x 64 bf16
+constexpr int MM_BN = 256;           // persistent kernel: columns of a pair's tile
+constexpr int MM_STAGES = 6;
+constexpr int MM_SMEM = 1024 + MM_STAGES * 2 * MM_TILE + 256;
+static_assert(2 * MM_STAGES + 6 <= 32, "barrier area");
+static_assert(MM_SMEM <= 232448, "shared memory per CTA");
 
 // ---------------------------------------------------------------- activations
 
@@ -110,39 +104,29 @@ __device__ __forceinline__ void act_grad_f(float x, int act, float& a, float& da
 
 // ---------------------------------------------------------------- row access
 
-// 32 bf16 values (16 packed words) to dst; ncols < 32 at the right edge.
-// Without vec (rows not 16-byte aligned) and in a group of 8 columns that the
-// edge cuts, one value at a time.
-__device__ __forceinline__ void store_row32(uint16_t* dst, const uint32_t (&pk)[16], int ncols,
-                                            bool vec) {
-  if (vec && ncols == 32) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      reinterpret_cast<uint4*>(dst)[j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+// 8 bf16 values (4 packed words) to dst; ncols < 8 at the right edge.  Without
+// vec (rows not 16-byte aligned) or at the edge, one value at a time.
+__device__ __forceinline__ void store8(uint16_t* dst, const uint32_t (&pk)[4], int ncols, bool vec) {
+  if (vec && ncols >= 8) {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if (2 * i < ncols) dst[2 * i] = static_cast<uint16_t>(pk[i]);
-    if (2 * i + 1 < ncols) dst[2 * i + 1] = static_cast<uint16_t>(pk[i] >> 16);
-  }
+  for (int i = 0; i < 8; ++i)
+    if (i < ncols) dst[i] = static_cast<uint16_t>(pk[i >> 1] >> (16 * (i & 1)));
 }
 
-__device__ __forceinline__ void load_row32(const uint16_t* src, uint32_t (&pk)[16], int ncols,
-                                           bool vec) {
-  if (vec && ncols == 32) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint4 v = *(reinterpret_cast<const uint4*>(src) + j);
-      pk[4 * j] = v.x;
-      pk[4 * j + 1] = v.y;
-      pk[4 * j + 2] = v.z;
-      pk[4 * j + 3] = v.w;
-    }
+__device__ __forceinline__ void load8(const uint16_t* src, uint32_t (&pk)[4], int ncols, bool vec) {
+  if (vec && ncols >= 8) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src);
+    pk[0] = v.x;
+    pk[1] = v.y;
+    pk[2] = v.z;
+    pk[3] = v.w;
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const uint32_t lo = 2 * i < ncols ? src[2 * i] : 0u;
     const uint32_t hi = 2 * i + 1 < ncols ? src[2 * i + 1] : 0u;
     pk[i] = lo | (hi << 16);
@@ -152,162 +136,194 @@ __device__ __forceinline__ void load_row32(const uint16_t* src, uint32_t (&pk)[1
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-template <bool PAIR>
+// "Accumulator buffer drained", to the even CTA of the pair.
 __device__ __forceinline__ void mm_tempty_signal(uint32_t addr) {
-  if (PAIR)
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-  else
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 // ---------------------------------------------------------------- epilogue
 
-// One accumulator tile: rows m0 .. m0 + 127 of this CTA, output columns from
-// n0.  Signals the accumulator buffer free after this warp's last TMEM read.
-template <bool PAIR, int BN, int EPI>
+// Output columns nb .. nb + 7 of row m from their fp32 sums v (and, for
+// MM_GATE, the up projection's u): the fused operation and the store.
+template <int EPI>
+__device__ __forceinline__ void mm_out8(const MmParams& p, int pr, int m, int nb, float (&v)[8],
+                                        const float (&u)[8]) {
+  const int N = p.N[pr], ncols = N - nb;
+  if (ncols <= 0) return;
+  uint32_t pk[4];
+  if constexpr (EPI == MM_LINEAR) {
+    const bool vec = p.vec != 0;
+    uint32_t b[4];
+    if (p.bias) {
+      load8(p.bias + nb, b, ncols, true);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] += bf16_lo(b[i]);
+        v[2 * i + 1] += bf16_hi(b[i]);
+      }
+    }
+    if (p.act == ACT_SILU) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = act_f(v[i], ACT_SILU);
+    } else if (p.act == ACT_GELU_TANH) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = act_f(v[i], ACT_GELU_TANH);
+    }
+    if (p.res) {
+      load8(p.res + static_cast<size_t>(m) * p.ld_res + nb, b, ncols, vec);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] += bf16_lo(b[i]);
+        v[2 * i + 1] += bf16_hi(b[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pk[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    store8(p.y[pr] + static_cast<size_t>(m) * p.ldy[pr] + nb, pk, ncols, vec);
+  } else if constexpr (EPI == MM_GATE) {
+    // the activation and the product in fp32, rounded once (F % 8 == 0: whole 16-byte groups)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      pk[i] = pack_bf16x2(act_f(v[2 * i], p.act) * u[2 * i], act_f(v[2 * i + 1], p.act) * u[2 * i + 1]);
+    store8(p.y[0] + static_cast<size_t>(m) * N + nb, pk, ncols, true);
+    if (p.gu) {
+      uint16_t* row = p.gu + static_cast<size_t>(m) * 2 * N + nb;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pk[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      store8(row, pk, ncols, true);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pk[i] = pack_bf16x2(u[2 * i], u[2 * i + 1]);
+      store8(row + N, pk, ncols, true);
+    }
+  } else {
+    uint32_t gg[4], uu[4];
+    const uint16_t* row = p.gu + static_cast<size_t>(m) * 2 * N + nb;
+    load8(row, gg, ncols, true);
+    load8(row + N, uu, ncols, true);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float u0 = bf16_lo(uu[i]), u1 = bf16_hi(uu[i]);
+      float a0, a1, e0, e1;
+      act_grad_f(bf16_lo(gg[i]), p.act, a0, e0);
+      act_grad_f(bf16_hi(gg[i]), p.act, a1, e1);
+      pk[i] = pack_bf16x2(a0 * u0, a1 * u1);
+      gg[i] = pack_bf16x2(v[2 * i] * u0 * e0, v[2 * i + 1] * u1 * e1);
+      uu[i] = pack_bf16x2(v[2 * i] * a0, v[2 * i + 1] * a1);
+    }
+    const size_t at = static_cast<size_t>(m) * N + nb;
+    store8(p.dg + at, gg, ncols, true);
+    store8(p.du + at, uu, ncols, true);
+    if (p.h) store8(p.h + at, pk, ncols, true);
+  }
+}
+
+// One accumulator tile of the persistent kernel: rows m0 .. m0 + 127 of this
+// CTA, output columns from n0.  Signals the accumulator buffer free after this
+// warp's last TMEM read.
+template <int EPI>
 __device__ __forceinline__ void mm_epilogue(const MmParams& p, int pr, uint32_t tacc, int m0, int n0,
                                             int quarter, int half, int lane, uint32_t tempty_addr) {
-  constexpr int W = EPI == MM_GATE ? BN / 2 : BN;   // output columns of a tile
+  constexpr int W = EPI == MM_GATE ? MM_BN / 2 : MM_BN;   // output columns of a tile
   constexpr int CH = W / 32;
   const int m = m0 + quarter * 32 + lane;
-  const int N = p.N[pr];
   const bool row_ok = m < p.M[pr];
-  const bool vec = p.vec != 0;
   const uint32_t t_row = tacc + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
   for (int c = half; c < CH; c += 2) {
     __syncwarp();
     uint32_t r[32];
     tmem_ld32(t_row + c * 32, r);
-    uint32_t r2[EPI == MM_GATE ? 32 : 1];
+    uint32_t r2[EPI == MM_GATE ? 32 : 8];
     if constexpr (EPI == MM_GATE) tmem_ld32(t_row + W + c * 32, r2);
     if (c + 2 >= CH) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mm_tempty_signal<PAIR>(tempty_addr);
+      if (lane == 0) mm_tempty_signal(tempty_addr);
     }
-    const int nb = n0 + c * 32;
-    if (!row_ok || nb >= N) continue;
-    const int ncols = min(32, N - nb);
-    if constexpr (EPI == MM_LINEAR) {
-      float v[32];
+    if (!row_ok) continue;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-      if (p.bias) {
-        uint32_t b[16];
-        load_row32(p.bias + nb, b, ncols, true);
+    for (int q = 0; q < 4; ++q) {
+      float v[8], u[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          v[2 * i] += bf16_lo(b[i]);
-          v[2 * i + 1] += bf16_hi(b[i]);
-        }
+      for (int i = 0; i < 8; ++i) {
+        v[i] = __uint_as_float(r[8 * q + i]);
+        u[i] = EPI == MM_GATE ? __uint_as_float(r2[8 * q + i]) : 0.f;
       }
-      if (p.act == ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = act_f(v[i], ACT_SILU);
-      } else if (p.act == ACT_GELU_TANH) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = act_f(v[i], ACT_GELU_TANH);
-      }
-      if (p.res) {
-        uint32_t b[16];
-        load_row32(p.res + static_cast<size_t>(m) * p.ld_res + nb, b, ncols, vec);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          v[2 * i] += bf16_lo(b[i]);
-          v[2 * i + 1] += bf16_hi(b[i]);
-        }
-      }
-      uint32_t pk[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-      store_row32(p.y[pr] + static_cast<size_t>(m) * p.ldy[pr] + nb, pk, ncols, vec);
-    } else if constexpr (EPI == MM_GATE) {
-      // the activation and the product in fp32, rounded once (F % 8 == 0: rows are 16-byte aligned)
-      uint32_t pk[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float a0 = act_f(__uint_as_float(r[2 * i]), p.act);
-        const float a1 = act_f(__uint_as_float(r[2 * i + 1]), p.act);
-        pk[i] = pack_bf16x2(a0 * __uint_as_float(r2[2 * i]), a1 * __uint_as_float(r2[2 * i + 1]));
-      }
-      store_row32(p.y[0] + static_cast<size_t>(m) * N + nb, pk, ncols, true);
-      if (p.gu) {
-        uint16_t* row = p.gu + static_cast<size_t>(m) * 2 * N + nb;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          pk[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-        store_row32(row, pk, ncols, true);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          pk[i] = pack_bf16x2(__uint_as_float(r2[2 * i]), __uint_as_float(r2[2 * i + 1]));
-        store_row32(row + N, pk, ncols, true);
-      }
-    } else {
-      uint32_t g[16], u[16], h[16];
-      const uint16_t* row = p.gu + static_cast<size_t>(m) * 2 * N + nb;
-      load_row32(row, g, ncols, true);
-      load_row32(row + N, u, ncols, true);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float d0 = __uint_as_float(r[2 * i]), d1 = __uint_as_float(r[2 * i + 1]);
-        const float u0 = bf16_lo(u[i]), u1 = bf16_hi(u[i]);
-        float a0, a1, e0, e1;
-        act_grad_f(bf16_lo(g[i]), p.act, a0, e0);
-        act_grad_f(bf16_hi(g[i]), p.act, a1, e1);
-        h[i] = pack_bf16x2(a0 * u0, a1 * u1);
-        g[i] = pack_bf16x2(d0 * u0 * e0, d1 * u1 * e1);
-        u[i] = pack_bf16x2(d0 * a0, d1 * a1);
-      }
-      const size_t at = static_cast<size_t>(m) * N + nb;
-      store_row32(p.dg + at, g, ncols, true);
-      store_row32(p.du + at, u, ncols, true);
-      if (p.h) store_row32(p.h + at, h, ncols, true);
+      mm_out8<EPI>(p, pr, m, n0 + c * 32 + q * 8, v, u);
     }
-  }
-  if (half >= CH) {   // narrow tiles: no chunk for this warp
-    __syncwarp();
-    if (lane == 0) mm_tempty_signal<PAIR>(tempty_addr);
   }
 }
 
-// Product and tile coordinates of a tile number.
-template <bool PAIR, int BN, int EPI>
+// Product and tile coordinates of a tile number, for tiles of BM rows and W columns.
+template <int BM, int W>
 __device__ __forceinline__ void mm_tile(const MmParams& p, int tile, int& pr, int& mt, int& nt) {
-  constexpr int BM = PAIR ? 256 : 128;
-  constexpr int W = EPI == MM_GATE ? BN / 2 : BN;
   pr = 0;
   while (pr < p.n_prob - 1 && tile >= p.tiles_end[pr]) ++pr;
   if (pr > 0) tile -= p.tiles_end[pr - 1];
   tile_coords(tile, (p.M[pr] + BM - 1) / BM, p.group_m[pr], (p.N[pr] + W - 1) / W, mt, nt);
 }
 
-// ---------------------------------------------------------------- kernel
+// The loads of one K block of a CTA: its 128 rows of A from row m0, and its 128
+// rows of B: from row n0, or with MM_GATE 64 or 128 rows of gate and / or up
+// (see the kernels).  `bar` counts the bytes.
+template <bool PAIR, bool MN>
+__device__ __forceinline__ void mm_load(const CUtensorMap* map, uint32_t bar, uint8_t* dst, int k, int row) {
+  if (MN) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) tma_load_2d_elect<PAIR>(map, bar, dst + i * 8192, row + 64 * i, k);
+  } else {
+    tma_load_2d_elect<PAIR>(map, bar, dst, k, row);
+  }
+}
 
-template <bool PAIR, int BN, bool AMN, bool BMN, int EPI>
+// The four MMAs of a K block: 16 values of K per instruction, 32 bytes of a
+// K-major row or 16 MN-major rows.
+template <bool PAIR, bool AMN, bool BMN>
+__device__ __forceinline__ void mm_block(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool first) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    umma_f16_elect<PAIR>(d_tmem, a + (static_cast<uint64_t>(k * (AMN ? 2048 : 32)) >> 4),
+                         b + (static_cast<uint64_t>(k * (BMN ? 2048 : 32)) >> 4), idesc, !first || k > 0);
+}
+
+template <bool MN>
+__device__ __forceinline__ uint64_t mm_desc(const uint8_t* tile) {
+  return MN ? umma_desc_mnmajor_sw128(smem_u32(tile), 8192) : umma_desc_kmajor_sw128(smem_u32(tile));
+}
+
+template <bool PAIR, bool AMN, bool BMN>
+constexpr uint32_t mm_idesc() {
+  return umma_idesc(false, PAIR ? 256 : 128, PAIR ? MM_BN : 128) | (AMN ? (1u << 15) : 0u) | (BMN ? (1u << 16) : 0u);
+}
+
+// ---------------------------------------------------------------- large products
+//
+// A pair of CTAs (one per SM) shares a 256 x 256 tile (cta_group::2): each
+// loads 128 rows of A and 128 rows of B, and the even CTA issues the MMAs for
+// both.  Persistent over tiles; the accumulator is double-buffered in TMEM, so
+// the epilogue of a tile overlaps the MMAs of the next.
+template <bool AMN, bool BMN, int EPI>
 __global__ void __launch_bounds__(MM_THREADS, 1)
     mm_kernel(const __grid_constant__ MmMaps maps, const __grid_constant__ MmParams p) {
-  using C = MmCfg<PAIR, BN>;
-  constexpr int STAGES = C::STAGES;
-  constexpr int W = EPI == MM_GATE ? BN / 2 : BN;
+  constexpr int STAGES = MM_STAGES;
+  constexpr int W = EPI == MM_GATE ? MM_BN / 2 : MM_BN;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint8_t* sA = smem;
-  uint8_t* sB = smem + STAGES * C::A_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE_BYTES);
-  uint64_t* full = bars;                     // [STAGES] (pair: even CTA's)
+  uint8_t* sB = smem + STAGES * MM_TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * 2 * MM_TILE);
+  uint64_t* full = bars;                     // [STAGES] (the even CTA's)
   uint64_t* empty = bars + STAGES;           // [STAGES]
   uint64_t* tfull = bars + 2 * STAGES;       // [2]
-  uint64_t* tempty = bars + 2 * STAGES + 2;  // [2] (pair: even CTA's)
+  uint64_t* tempty = bars + 2 * STAGES + 2;  // [2] (the even CTA's)
   uint64_t* drain = bars + 2 * STAGES + 4;   // MMA drain on the error path
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int rank = PAIR ? static_cast<int>(cluster_rank()) : 0;
-  const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x;
-  const int workers = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const int rank = static_cast<int>(cluster_rank());
+  const int worker = blockIdx.x >> 1, workers = gridDim.x >> 1;
   const int num_tiles = p.tiles_end[p.n_prob - 1];
 
   if (threadIdx.x == 0) {
@@ -317,27 +333,21 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], (PAIR ? 2 : 1) * MM_EPI_WARPS);
+      mbar_init(&tempty[a], 2 * MM_EPI_WARPS);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&maps.a[0]);
-    prefetch_tmap(&maps.b[0]);
+    prefetch_tmap(&maps.b[EPI == MM_GATE ? rank : 0]);
   }
   if (warp == 1) {
-    if (PAIR) {
-      tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(tmem_slot, C::TMEM_COLS);
-      tmem_relinquish();
-    }
+    tmem_alloc_pair(tmem_slot, 2 * MM_BN);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
-  if (PAIR) cluster_sync_all();
-  else __syncthreads();
+  cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();
@@ -345,73 +355,53 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer (the whole warp, one lane issues)
-    {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int tile = worker; tile < num_tiles && ok; tile += workers) {
-        int pr, mt, nt;
-        mm_tile<PAIR, BN, EPI>(p, tile, pr, mt, nt);
-        const int m0 = mt * (PAIR ? 256 : 128) + rank * 128;
-        const int num_kb = p.num_kb[pr];
-        for (int seg = 0; seg < p.segs && ok; ++seg) {   // segs == 2 only for a single product
-          const CUtensorMap* ma = &maps.a[pr + seg];
-          const CUtensorMap* mb = &maps.b[EPI == MM_GATE ? rank : pr + seg];
-          for (int kb = 0; kb < num_kb; ++kb) {
-            if (!mbar_wait_warp(&empty[stage], phase ^ 1u, p.status)) { ok = false; break; }
-            const int k = kb * 64;
-            uint8_t* da = sA + stage * C::A_BYTES;
-            uint8_t* db = sB + stage * C::B_BYTES;
-            const uint32_t fb = PAIR ? mapa_shared(smem_u32(&full[stage]), 0) : smem_u32(&full[stage]);
-            if (rank == 0) mbar_expect_elect(&full[stage], (PAIR ? 2 : 1) * C::STAGE_BYTES);
-            if (AMN) {
-#pragma unroll
-              for (int i = 0; i < 2; ++i) tma_load_2d_elect<PAIR>(ma, fb, da + i * 8192, m0 + 64 * i, k);
-            } else {
-              tma_load_2d_elect<PAIR>(ma, fb, da, k, m0);
-            }
-            if (EPI == MM_GATE) {
-              tma_load_2d_elect<PAIR>(mb, fb, db, k, nt * W);
-              if (!PAIR) tma_load_2d_elect<PAIR>(&maps.b[1], fb, db + C::B_BYTES / 2, k, nt * W);
-            } else if (BMN) {
-#pragma unroll
-              for (int i = 0; i < C::B_ROWS / 64; ++i)
-                tma_load_2d_elect<PAIR>(mb, fb, db + i * 8192, nt * BN + rank * C::B_ROWS + 64 * i, k);
-            } else {
-              tma_load_2d_elect<PAIR>(mb, fb, db, k, nt * BN + rank * C::B_ROWS);
-            }
-            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-          }
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = worker; tile < num_tiles && ok; tile += workers) {
+      int pr, mt, nt;
+      mm_tile<256, W>(p, tile, pr, mt, nt);
+      const int m0 = mt * 256 + rank * 128;
+      const int n0 = EPI == MM_GATE ? nt * W : nt * MM_BN + rank * 128;
+      const int num_kb = p.num_kb[pr];
+      for (int seg = 0; seg < p.segs && ok; ++seg) {   // segs == 2 only for a single product
+        const CUtensorMap* ma = &maps.a[pr + seg];
+        const CUtensorMap* mb = &maps.b[EPI == MM_GATE ? rank : pr + seg];
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!mbar_wait_warp(&empty[stage], phase ^ 1u, p.status)) { ok = false; break; }
+          const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+          if (rank == 0) mbar_expect_elect(&full[stage], 4 * MM_TILE);
+          mm_load<true, AMN>(ma, fb, sA + stage * MM_TILE, kb * 64, m0);
+          mm_load<true, BMN>(mb, fb, sB + stage * MM_TILE, kb * 64, n0);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      if (!ok) {
-        // Error path: the loads in flight must land before the CTA exits.  The
-        // CTA that armed the full barriers waits (bounded) on them; the odd CTA
-        // of a pair, which cannot, gives its last loads a fixed 200 us.
-        if (rank == 0) {
-          for (int s = 0; s < STAGES; ++s) {
-            const uint32_t par = (s < stage) ? phase : (phase ^ 1u);
-            const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(&full[s], par) && globaltimer_ns() - t0 < QI_WAIT_NS) {
-            }
-          }
-        } else {
+    }
+    if (!ok) {
+      // Error path: the loads in flight must land before the CTA exits.  The
+      // even CTA, which armed the full barriers, waits (bounded) on them; the
+      // odd one, which cannot, gives its last loads a fixed 200 us.
+      if (rank == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+          const uint32_t par = (s < stage) ? phase : (phase ^ 1u);
           const uint64_t t0 = globaltimer_ns();
-          while (globaltimer_ns() - t0 < 200000ull) {
+          while (!mbar_try_wait(&full[s], par) && globaltimer_ns() - t0 < QI_WAIT_NS) {
           }
+        }
+      } else {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000ull) {
         }
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (pair: even CTA)
+    // ------------------------------------------------------------ MMA issuer (even CTA)
     // The whole warp runs the loop and one elected lane issues: operands that
     // are uniform over a converged warp reach the tensor core's instruction
     // without a move per lane (an MMA issued under a lane test took 54 clocks).
     if (rank == 0) {
-      constexpr uint32_t idesc = umma_idesc(false, PAIR ? 256 : 128, BN) | (AMN ? (1u << 15) : 0u) |
-                                 (BMN ? (1u << 16) : 0u);
-      const uint64_t adesc0 = AMN ? umma_desc_mnmajor_sw128(smem_u32(sA), 8192) : umma_desc_kmajor_sw128(smem_u32(sA));
-      const uint64_t bdesc0 = BMN ? umma_desc_mnmajor_sw128(smem_u32(sB), 8192) : umma_desc_kmajor_sw128(smem_u32(sB));
+      constexpr uint32_t idesc = mm_idesc<true, AMN, BMN>();
+      const uint64_t adesc = mm_desc<AMN>(sA), bdesc = mm_desc<BMN>(sB);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -419,36 +409,27 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
       bool ok = true;
       for (int tile = worker; tile < num_tiles && ok; tile += workers) {
         int pr, mt, nt;
-        mm_tile<PAIR, BN, EPI>(p, tile, pr, mt, nt);
+        mm_tile<256, W>(p, tile, pr, mt, nt);
         const int total_kb = p.num_kb[pr] * p.segs;
-        const bool free = PAIR ? mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, p.status)
-                               : mbar_wait(&tempty[acc], acc_phase ^ 1u, p.status);
-        if (!__all_sync(0xffffffffu, free)) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, p.status))) { ok = false; break; }
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * MM_BN);
         for (int kb = 0; kb < total_kb; ++kb) {
           if (!mbar_wait_warp(&full[stage], phase, p.status)) { ok = false; break; }
           tc_fence_after();
-          const uint64_t adesc = adesc0 + static_cast<uint64_t>(stage * (C::A_BYTES >> 4));
-          const uint64_t bdesc = bdesc0 + static_cast<uint64_t>(stage * (C::B_BYTES >> 4));
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {   // 16 values of K per instruction: 32 bytes of a K-major row, 16 MN-major rows
-            const uint64_t ao = static_cast<uint64_t>(k * (AMN ? 2048 : 32)) >> 4;
-            const uint64_t bo = static_cast<uint64_t>(k * (BMN ? 2048 : 32)) >> 4;
-            umma_f16_elect<PAIR>(d_tmem, adesc + ao, bdesc + bo, idesc, (kb | k) != 0);
-          }
-          umma_commit_elect<PAIR>(&empty[stage]);
+          const uint64_t off = static_cast<uint64_t>(stage * (MM_TILE >> 4));
+          mm_block<true, AMN, BMN>(d_tmem, adesc + off, bdesc + off, idesc, kb == 0);
+          umma_commit_elect<true>(&empty[stage]);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        umma_commit_elect<PAIR>(&tfull[acc]);
+        umma_commit_elect<true>(&tfull[acc]);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
       if (!ok) {
         // make sure no MMA is still writing TMEM before it is released
-        if (PAIR) umma_commit_elect<true>(drain, 0x1);
-        else umma_commit_elect<false>(drain);
+        umma_commit_elect<true>(drain, 0x1);
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < QI_WAIT_NS) {
         }
@@ -462,13 +443,11 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     uint32_t acc_phase = 0;
     for (int tile = worker; tile < num_tiles; tile += workers) {
       int pr, mt, nt;
-      mm_tile<PAIR, BN, EPI>(p, tile, pr, mt, nt);
-      const int m0 = mt * (PAIR ? 256 : 128) + rank * 128;
+      mm_tile<256, W>(p, tile, pr, mt, nt);
       if (!mbar_wait_warp(&tfull[acc], acc_phase, p.status)) break;
       tc_fence_after();
-      const uint32_t te = PAIR ? mapa_shared(smem_u32(&tempty[acc]), 0) : smem_u32(&tempty[acc]);
-      mm_epilogue<PAIR, BN, EPI>(p, pr, tmem_base + static_cast<uint32_t>(acc * BN), m0, nt * W,
-                                 quarter, half, lane, te);
+      mm_epilogue<EPI>(p, pr, tmem_base + static_cast<uint32_t>(acc * MM_BN), mt * 256 + rank * 128, nt * W,
+                       quarter, half, lane, mapa_shared(smem_u32(&tempty[acc]), 0));
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
@@ -477,13 +456,223 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   // Neither CTA of a pair leaves (or frees TMEM) while the other may still read
   // its shared memory, arrive on its barriers, or have MMAs writing its TMEM.
   tc_fence_before();
-  if (PAIR) cluster_sync_all();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 2 * MM_BN);
+  }
+}
+
+// ---------------------------------------------------------------- middle sizes
+//
+// Too few 256 x 256 tiles to fill the GPU: K is shared as well.  A cluster
+// computes one tile, its S parts each over a part of K: S pairs of CTAs on a
+// 256 x 256 tile (PAIR), or S single CTAs on a 128 x 128 tile when there are
+// at most 128 rows (two CTAs per SM then, so one's loads and MMAs lie under
+// the other's start and end).  When its MMAs are done, a CTA puts its fp32
+// sums into its shared memory; after a cluster barrier every CTA adds up a
+// share of the columns over the S parts' shared memory, in the order of K,
+// and runs the epilogue on them.  Nothing goes through memory and the result
+// does not depend on timing.
+// The sums lie as [groups of 4 columns][128 rows] of float4: the lanes of a
+// warp hold consecutive rows and touch 512 contiguous bytes.
+template <bool PAIR>
+struct MsCfg {
+  static constexpr int STAGES = PAIR ? 6 : 3;
+  static constexpr int COLS = PAIR ? 256 : 128;   // accumulator columns
+  static constexpr int SMEM = 1024 + STAGES * 2 * MM_TILE + 256;
+  static_assert(PAIR || 2 * (SMEM + 1024) <= 233472, "two CTAs per SM");
+  static_assert(128 * COLS * 4 <= STAGES * 2 * MM_TILE, "the sums over the stages");
+};
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+template <bool PAIR, bool AMN, bool BMN, int EPI>
+__global__ void __launch_bounds__(MM_THREADS, PAIR ? 1 : 2)
+    mm_split_kernel(const __grid_constant__ MmMaps maps, const __grid_constant__ MmParams p, const int S) {
+  using C = MsCfg<PAIR>;
+  constexpr int STAGES = C::STAGES;
+  constexpr int BM = PAIR ? 256 : 128;
+  constexpr int W = EPI == MM_GATE ? C::COLS / 2 : C::COLS;   // output columns of a tile
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + STAGES * MM_TILE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * 2 * MM_TILE);   // [STAGES] (pair: even CTA's)
+  uint64_t* empty = full + STAGES;                                             // [STAGES]
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* drain = tfull + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int ctas = PAIR ? 2 * S : S;   // of the cluster
+  const uint32_t crank = ctas > 1 ? cluster_rank() : 0u;
+  const uint32_t even = PAIR ? crank & ~1u : crank;          // the CTA that issues this one's MMAs
+  const int rank = PAIR ? static_cast<int>(crank & 1u) : 0;  // half of the tile's rows
+  const int part = static_cast<int>(PAIR ? crank >> 1 : crank);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    if (PAIR) {
+      tmem_alloc_pair(tmem_slot, C::COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, C::COLS);
+      tmem_relinquish();
+    }
+  }
+  int pr, mt, nt;
+  mm_tile<BM, W>(p, static_cast<int>(blockIdx.x) / ctas, pr, mt, nt);
+  const int total_kb = p.num_kb[pr] * p.segs;
+  const int lo = total_kb * part / S, hi = total_kb * (part + 1) / S;
+  const int m0 = mt * BM + rank * 128;
+  const int n0 = EPI == MM_GATE ? nt * W : nt * W + rank * 128;   // first row of B of this CTA
+  tc_fence_before();
+  if (PAIR) cluster_sync_all();   // barriers of both CTAs initialised before any remote arrive
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  bool ok = true;
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (the whole warp, one lane issues)
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = lo; kb < hi; ++kb) {
+      if (!mbar_wait_warp(&empty[stage], phase ^ 1u, p.status)) { ok = false; break; }
+      const int seg = kb >= p.num_kb[pr] ? 1 : 0;   // segs == 2 only for a single product
+      const int k = (kb - seg * p.num_kb[pr]) * 64;
+      const uint32_t fb = PAIR ? mapa_shared(smem_u32(&full[stage]), even) : smem_u32(&full[stage]);
+      if (rank == 0) mbar_expect_elect(&full[stage], (PAIR ? 4 : 2) * MM_TILE);
+      mm_load<PAIR, AMN>(&maps.a[pr + seg], fb, sA + stage * MM_TILE, k, m0);
+      if (EPI == MM_GATE && !PAIR) {
+        mm_load<PAIR, false>(&maps.b[0], fb, sB + stage * MM_TILE, k, n0);
+        mm_load<PAIR, false>(&maps.b[1], fb, sB + stage * MM_TILE + MM_TILE / 2, k, n0);
+      } else {
+        mm_load<PAIR, BMN>(&maps.b[EPI == MM_GATE ? rank : pr + seg], fb, sB + stage * MM_TILE, k, n0);
+      }
+      if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+    }
+    if (!ok) {   // the loads in flight must land before the CTA exits (see mm_kernel)
+      if (rank == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+          const uint32_t par = (s < stage) ? phase : (phase ^ 1u);
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(&full[s], par) && globaltimer_ns() - t0 < QI_WAIT_NS) {
+          }
+        }
+      } else {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (pair: even CTA)
+    if (rank == 0) {
+      constexpr uint32_t idesc = mm_idesc<PAIR, AMN, BMN>();
+      const uint64_t adesc = mm_desc<AMN>(sA), bdesc = mm_desc<BMN>(sB);
+      const uint16_t both = static_cast<uint16_t>(0x3u << even);
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = lo; kb < hi; ++kb) {
+        if (!mbar_wait_warp(&full[stage], phase, p.status)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t off = static_cast<uint64_t>(stage * (MM_TILE >> 4));
+        mm_block<PAIR, AMN, BMN>(tmem_base, adesc + off, bdesc + off, idesc, kb == lo);
+        umma_commit_elect<PAIR>(&empty[stage], both);
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+      if (ok) {
+        umma_commit_elect<PAIR>(tfull, both);
+      } else {
+        umma_commit_elect<PAIR>(drain, static_cast<uint16_t>(0x1u << even));
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < QI_WAIT_NS) {
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ this CTA's sums into its shared memory
+    // (every MMA of the pair, and so every load, is done with the stages)
+    const int quarter = warp & 3, half = (warp - 2) >> 2, row = quarter * 32 + lane;
+    float4* sums = reinterpret_cast<float4*>(smem);
+    ok = mbar_wait_warp(tfull, 0, p.status);
+    tc_fence_after();
+    const bool none = lo == hi;   // no K block for this part: TMEM was not written
+    if (ok)
+#pragma unroll 1
+      for (int c = half * (C::COLS / 64); c < (half + 1) * (C::COLS / 64); ++c) {
+        uint32_t r[32];
+        tmem_ld32(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + c * 32, r);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          sums[(c * 8 + q) * 128 + row] =
+              none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                   : make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                 __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+      }
+  }
+  tc_fence_before();
+  if (ctas > 1) cluster_sync_all();
   else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    if (PAIR) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
-    else tmem_dealloc(tmem_base, C::TMEM_COLS);
+    if (PAIR) tmem_dealloc_pair(tmem_base, C::COLS);
+    else tmem_dealloc(tmem_base, C::COLS);
   }
+  if (warp >= 2 && ok) {
+    // columns [part W / S, + W / S) of this CTA's rows, half of them per thread
+    const int et = threadIdx.x - 64, row = et & 127, per = W / S / 2;
+    const int m = m0 + row, c0 = part * (W / S) + (et >> 7) * per;
+    const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(row) * 16;
+    if (m < p.M[pr])
+#pragma unroll 1
+      for (int c = c0; c < c0 + per; c += 8) {
+        float v[8], u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.f;
+#pragma unroll 1
+        for (int s = 0; s < S; ++s) {
+          const uint32_t peer = static_cast<uint32_t>(PAIR ? 2 * s + rank : s);
+          const uint32_t from = (ctas > 1 ? mapa_shared(mine, peer) : mine) + (c >> 2) * 2048;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float4 x = ld_cluster4(from + e * 2048);
+            v[4 * e] += x.x;
+            v[4 * e + 1] += x.y;
+            v[4 * e + 2] += x.z;
+            v[4 * e + 3] += x.w;
+            if (EPI == MM_GATE) {
+              const float4 y = ld_cluster4(from + (W / 4 + e) * 2048);   // the up columns, W further on
+              u[4 * e] += y.x;
+              u[4 * e + 1] += y.y;
+              u[4 * e + 2] += y.z;
+              u[4 * e + 3] += y.w;
+            }
+          }
+        }
+        mm_out8<EPI>(p, pr, m, nt * W + c, v, u);
+      }
+  }
+  if (ctas > 1) cluster_sync_all();   // no CTA leaves while another may read its sums
 }
 
 // ---------------------------------------------------------------- few rows
@@ -513,9 +702,20 @@ struct SkinnyParams {
   uint16_t* gu;           // GATE: optional [M, 2N]
 };
 
+// 16 bytes of a weight row: read once, not kept in L1.
+__device__ __forceinline__ uint4 ld_stream16(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 template <int NT, bool GATE>
-__global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const SkinnyParams p) {
+__global__ void __launch_bounds__(SK_THREADS, 2) skinny_kernel(const SkinnyParams p) {
   constexpr int MATS = GATE ? 2 : 1;
+  constexpr int U = GATE ? 1 : 2;   // 64-wide pieces of K per batch of loads: 8 loads of weights
+  constexpr int STEP = SK_THREADS / 32 * 64;
   __shared__ float red[SK_THREADS / 32][MATS][NT * 8][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -528,8 +728,6 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const SkinnyParams p
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-  pdl_wait();
-  pdl_trigger();
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const uint16_t* wr[MATS][2];
   wr[0][0] = p.w + static_cast<size_t>(r0) * p.K;
@@ -541,27 +739,52 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const SkinnyParams p
   const uint16_t* ar[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) ar[j] = p.a + static_cast<size_t>(min(8 * j + g, p.M - 1)) * p.lda;
-#pragma unroll 4
-  for (int kb = warp * 64; kb < p.K; kb += SK_THREADS / 32 * 64) {
+  // two batches of loads in turn: one is on its way while the other is multiplied
+  struct Batch {
+    uint4 w[U][2][MATS][2], x[U][2][NT];
+  };
+  auto load = [&](Batch& q, int kb) {
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-      const int k = kb + 32 * sub + 8 * t;   // K % 8 == 0: a chunk of 8 lies inside or outside
-      const bool in = k < p.K;
-      uint4 w[MATS][2], x[NT];
+    for (int b = 0; b < U; ++b)
 #pragma unroll
-      for (int i = 0; i < MATS; ++i)
+      for (int sub = 0; sub < 2; ++sub) {
+        const int k = kb + b * STEP + 32 * sub + 8 * t;   // K % 8 == 0: a chunk of 8 lies inside or outside
+        const bool in = k < p.K;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) w[i][e] = in ? __ldg(reinterpret_cast<const uint4*>(wr[i][e] + k)) : zero;
+        for (int i = 0; i < MATS; ++i)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        x[j] = in && 8 * j + g < p.M ? *reinterpret_cast<const uint4*>(ar[j] + k) : zero;
+          for (int e = 0; e < 2; ++e) q.w[b][sub][i][e] = in ? ld_stream16(wr[i][e] + k) : zero;
 #pragma unroll
-      for (int i = 0; i < MATS; ++i)
+        for (int j = 0; j < NT; ++j)
+          q.x[b][sub][j] = in && 8 * j + g < p.M ? *reinterpret_cast<const uint4*>(ar[j] + k) : zero;
+      }
+  };
+  auto multiply = [&](const Batch& q) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          mma_16816(acc[i][j], w[i][0].x, w[i][1].x, w[i][0].y, w[i][1].y, x[j].x, x[j].y);
-          mma_16816(acc[i][j], w[i][0].z, w[i][1].z, w[i][0].w, w[i][1].w, x[j].z, x[j].w);
-        }
+    for (int b = 0; b < U; ++b)
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+        for (int i = 0; i < MATS; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const uint4 w0 = q.w[b][sub][i][0], w1 = q.w[b][sub][i][1], x = q.x[b][sub][j];
+            mma_16816(acc[i][j], w0.x, w1.x, w0.y, w1.y, x.x, x.y);
+            mma_16816(acc[i][j], w0.z, w1.z, w0.w, w1.w, x.z, x.w);
+          }
+  };
+  pdl_wait();
+  pdl_trigger();
+  {
+    Batch q0, q1;
+    int kb = warp * 64;
+    load(q0, kb);
+#pragma unroll 1
+    for (; kb < p.K; kb += 2 * U * STEP) {
+      load(q1, kb + U * STEP);
+      multiply(q0);
+      load(q0, kb + 2 * U * STEP);
+      multiply(q1);
     }
   }
 #pragma unroll
@@ -622,64 +845,6 @@ static bool mm_map(CUtensorMap* m, const MmOperand& o, bool mn, int box_rows) {
                       static_cast<uint32_t>(mn ? 64 : box_rows));
 }
 
-template <bool PAIR, int BN, bool AMN, bool BMN, int EPI>
-static int mm_launch(const MmOperand* A, const MmOperand* B, int n_ops_a, int n_ops_b, MmParams p,
-                     int num_sms, cudaStream_t st) {
-  using C = MmCfg<PAIR, BN>;
-  auto kern = mm_kernel<PAIR, BN, AMN, BMN, EPI>;
-  static std::atomic<uint64_t> done{0};
-  if (!allow_smem(kern, C::SMEM, done)) {
-    launch_result();
-    return -1;
-  }
-  MmMaps maps;
-  for (int i = 0; i < MM_MAX_PROB; ++i) {
-    if (!mm_map(&maps.a[i], A[i < n_ops_a ? i : 0], AMN, 128)) return -2;
-    if (!mm_map(&maps.b[i], B[i < n_ops_b ? i : 0], BMN, EPI == MM_GATE ? BN / 2 : C::B_ROWS)) return -2;
-  }
-  constexpr int BM = PAIR ? 256 : 128;
-  constexpr int W = EPI == MM_GATE ? BN / 2 : BN;
-  int tiles = 0;
-  for (int i = 0; i < p.n_prob; ++i) {
-    const int mt = (p.M[i] + BM - 1) / BM;
-    tiles += mt * ((p.N[i] + W - 1) / W);
-    p.tiles_end[i] = tiles;
-    p.group_m[i] = mt < 8 ? mt : 8;
-  }
-  const int cap = PAIR ? num_sms / 2 : num_sms;
-  const int workers = tiles < cap ? tiles : cap;
-  launch_pdl(kern, dim3(PAIR ? 2 * workers : workers), dim3(MM_THREADS), C::SMEM, st, PAIR ? 2 : 1,
-             maps, p);
-  return launch_result();
-}
-
-// Tile shape of a launch: the one whose rounds of tiles cost least.  A 64-wide
-// K block takes a CTA about 512 clocks in a pair's 256 x 256 tile (the tensor
-// pipe) and is bound by the operand bytes an SM can take in (about 64 a clock)
-// in the narrower tiles of one CTA.
-enum MmShape { MM_PAIR256 = 0, MM_S128 = 1, MM_S64 = 2, MM_S32 = 3 };
-static MmShape mm_shape(const MmParams& p, int w_div, int num_sms, int narrowest) {
-  static const int bm[4] = {256, 128, 128, 128}, bn[4] = {256, 128, 64, 32};
-  static const int clocks[4] = {512, 512, 384, 320};
-  long best = 0;
-  int pick = 0;
-  for (int s = 0; s <= narrowest; ++s) {
-    long tiles = 0, kb = 0;
-    for (int i = 0; i < p.n_prob; ++i) {
-      const int w = bn[s] / w_div;
-      tiles += static_cast<long>((p.M[i] + bm[s] - 1) / bm[s]) * ((p.N[i] + w - 1) / w);
-      kb = kb > p.num_kb[i] * p.segs ? kb : p.num_kb[i] * p.segs;
-    }
-    const long cap = s == MM_PAIR256 ? num_sms / 2 : num_sms;
-    const long cost = ((tiles + cap - 1) / cap) * kb * clocks[s];
-    if (s == 0 || cost < best) {
-      best = cost;
-      pick = s;
-    }
-  }
-  return static_cast<MmShape>(pick);
-}
-
 static MmParams mm_params(int* status) {
   MmParams p;
   memset(&p, 0, sizeof(p));
@@ -688,6 +853,137 @@ static MmParams mm_params(int* status) {
   p.vec = 1;
   p.status = status;
   return p;
+}
+
+static long mm_count_tiles(MmParams& p, int bm, int w) {
+  long tiles = 0;
+  for (int i = 0; i < p.n_prob; ++i) {
+    const int mt = (p.M[i] + bm - 1) / bm;
+    tiles += static_cast<long>(mt) * ((p.N[i] + w - 1) / w);
+    p.tiles_end[i] = static_cast<int>(tiles);
+    p.group_m[i] = mt < 8 ? mt : 8;
+  }
+  return tiles;
+}
+
+// Clusters of `ctas` CTAs of a kernel that run at the same time on the current
+// device (the SMs of one GPC hold a whole number of clusters: 74, 33 and 15
+// clusters of 2, 4 and 8 on 148 SMs), asked once per device.
+template <class K>
+static int cluster_places(K kern, int ctas, int smem, int num_sms) {
+  if (ctas <= 1) return num_sms;
+  static std::atomic<int> known[64][4];   // per kernel instantiation; 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return num_sms / ctas;
+  const int slot = ctas == 2 ? 0 : (ctas == 4 ? 1 : 2);
+  const bool keep = dev < 64;
+  int n = keep ? known[dev][slot].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    cfg.blockDim = dim3(MM_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = num_sms / ctas;
+    }
+    if (keep) known[dev][slot].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Kernel of a launch.  The estimate is in clocks: rounds of tiles times K
+// blocks times the clocks of a block, plus about 15000 for what starts and ends
+// a tile (the launch, the first loads, the sums' way out; the persistent kernel
+// pays it once).  A K block of a pair's tile takes about 600 clocks (32 KB into
+// each SM); one of a 128 x 128 tile about as long, for half the work per SM.
+// Measured, whole K / parts of K: 64 x 4096 x 4096 15.2 / 12.7 us, 64 x
+// 4096 x 11008 34 / 23 us, 512 x 4096 x 11008 55 / 38 us.
+struct MmShape {
+  bool pair;
+  int S;   // parts of K (pair with 1: the persistent kernel)
+};
+template <bool AMN, bool BMN, int EPI>
+static bool mm_shape(MmParams p, int num_sms, MmShape* pick) {
+  constexpr int W_DIV = EPI == MM_GATE ? 2 : 1;
+  static std::atomic<uint64_t> done_p{0}, done_s{0};
+  auto pair_kern = mm_split_kernel<true, AMN, BMN, EPI>;
+  auto single_kern = mm_split_kernel<false, AMN, BMN, EPI>;
+  if (!allow_smem(pair_kern, MsCfg<true>::SMEM, done_p) || !allow_smem(single_kern, MsCfg<false>::SMEM, done_s))
+    return false;
+  long kb = 0, rows = 0;
+  for (int i = 0; i < p.n_prob; ++i) {
+    kb = kb > p.num_kb[i] * p.segs ? kb : p.num_kb[i] * p.segs;
+    rows = rows > p.M[i] ? rows : p.M[i];
+  }
+  auto rounds = [](long n, long places) { return (n + places - 1) / places; };
+  const long tiles = mm_count_tiles(p, 256, 256 / W_DIV);
+  long best = rounds(tiles, num_sms / 2) * kb * 600 + 14000;
+  *pick = {true, 1};
+  for (int s = 2; s <= 4; s *= 2) {
+    const long cost = rounds(tiles, cluster_places(pair_kern, 2 * s, MsCfg<true>::SMEM, num_sms)) *
+                          (rounds(kb, s) * 600 + 15000);
+    if (cost < best) {
+      best = cost;
+      *pick = {true, s};
+    }
+  }
+  if (rows <= 128) {
+    const long t1 = mm_count_tiles(p, 128, 128 / W_DIV);
+    for (int s = 1; s <= (EPI == MM_GATE ? 4 : 8); s *= 2) {
+      const long cost = rounds(t1, cluster_places(single_kern, s, MsCfg<false>::SMEM, num_sms)) *
+                            (rounds(kb, s) * (500 + 100 * rows / 128) + 15000);
+      if (cost < best) {
+        best = cost;
+        *pick = {false, s};
+      }
+    }
+  }
+  return true;
+}
+
+template <bool PAIR, bool AMN, bool BMN, int EPI>
+static int mm_launch_split(const MmMaps& maps, MmParams p, int S, cudaStream_t st) {
+  auto kern = mm_split_kernel<PAIR, AMN, BMN, EPI>;
+  const long tiles = mm_count_tiles(p, PAIR ? 256 : 128, MsCfg<PAIR>::COLS / (EPI == MM_GATE ? 2 : 1));
+  const unsigned ctas = static_cast<unsigned>(PAIR ? 2 * S : S);
+  launch_pdl(kern, dim3(static_cast<unsigned>(tiles) * ctas), dim3(MM_THREADS), MsCfg<PAIR>::SMEM, st, ctas, maps, p, S);
+  return launch_result();
+}
+
+template <bool AMN, bool BMN, int EPI>
+static int mm_launch(const MmOperand* A, const MmOperand* B, int n_ops_a, int n_ops_b, MmParams p,
+                     int num_sms, cudaStream_t st) {
+  constexpr int W_DIV = EPI == MM_GATE ? 2 : 1;
+  MmShape shape;
+  if (!mm_shape<AMN, BMN, EPI>(p, num_sms, &shape)) {
+    launch_result();
+    return -1;
+  }
+  MmMaps maps;
+  for (int i = 0; i < MM_MAX_PROB; ++i) {
+    if (!mm_map(&maps.a[i], A[i < n_ops_a ? i : 0], AMN, 128)) return -2;
+    if (!mm_map(&maps.b[i], B[i < n_ops_b ? i : 0], BMN, !shape.pair && EPI == MM_GATE ? 64 : 128)) return -2;
+  }
+  if (!shape.pair) return mm_launch_split<false, AMN, BMN, EPI>(maps, p, shape.S, st);
+  if (shape.S > 1) return mm_launch_split<true, AMN, BMN, EPI>(maps, p, shape.S, st);
+  auto kern = mm_kernel<AMN, BMN, EPI>;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(kern, MM_SMEM, done)) {
+    launch_result();
+    return -1;
+  }
+  const long tiles = mm_count_tiles(p, 256, MM_BN / W_DIV);
+  const int workers = static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
+  launch_pdl(kern, dim3(2 * workers), dim3(MM_THREADS), MM_SMEM, st, 2, maps, p);
+  return launch_result();
 }
 
 constexpr int SK_MAX_ROWS = 16;
@@ -725,13 +1021,7 @@ int launch_linear_act(const LinearActParams& q, cudaStream_t st) {
   p.ld_res = q.ld_res;
   p.vec = rows16(q.y, q.ldy) && (!q.res || rows16(q.res, q.ld_res));
   const MmOperand a{q.a, q.M, q.K, q.lda}, b{q.w, q.N, q.K, q.K};
-  switch (mm_shape(p, 1, q.num_sms, MM_S32)) {
-    case MM_PAIR256: return mm_launch<true, 256, false, false, MM_LINEAR>(&a, &b, 1, 1, p, q.num_sms, st);
-    case MM_S128: return mm_launch<false, 128, false, false, MM_LINEAR>(&a, &b, 1, 1, p, q.num_sms, st);
-    case MM_S64: return mm_launch<false, 64, false, false, MM_LINEAR>(&a, &b, 1, 1, p, q.num_sms, st);
-    case MM_S32: return mm_launch<false, 32, false, false, MM_LINEAR>(&a, &b, 1, 1, p, q.num_sms, st);
-  }
-  return -1;
+  return mm_launch<false, false, MM_LINEAR>(&a, &b, 1, 1, p, q.num_sms, st);
 }
 
 int launch_gate_up(const GateUpParams& q, cudaStream_t st) {
@@ -751,12 +1041,7 @@ int launch_gate_up(const GateUpParams& q, cudaStream_t st) {
   p.gu = q.gu;
   const MmOperand a{q.x, q.M, q.H, q.ldx};
   const MmOperand b[2] = {{q.gate, q.F, q.H, q.H}, {q.up, q.F, q.H, q.H}};
-  switch (mm_shape(p, 2, q.num_sms, MM_S64)) {
-    case MM_PAIR256: return mm_launch<true, 256, false, false, MM_GATE>(&a, b, 1, 2, p, q.num_sms, st);
-    case MM_S128: return mm_launch<false, 128, false, false, MM_GATE>(&a, b, 1, 2, p, q.num_sms, st);
-    case MM_S64: return mm_launch<false, 64, false, false, MM_GATE>(&a, b, 1, 2, p, q.num_sms, st);
-    default: return -1;
-  }
+  return mm_launch<false, false, MM_GATE>(&a, b, 1, 2, p, q.num_sms, st);
 }
 
 int launch_gated_dh(const GatedBackwardParams& q, cudaStream_t st) {
@@ -770,12 +1055,7 @@ int launch_gated_dh(const GatedBackwardParams& q, cudaStream_t st) {
   p.du = q.du;
   p.h = q.ddown ? q.h : nullptr;
   const MmOperand a{q.dy, q.M, q.H, q.ld_dy}, b{q.down, q.H, q.F, q.F};
-  switch (mm_shape(p, 1, q.num_sms, MM_S64)) {
-    case MM_PAIR256: return mm_launch<true, 256, false, true, MM_DGATE>(&a, &b, 1, 1, p, q.num_sms, st);
-    case MM_S128: return mm_launch<false, 128, false, true, MM_DGATE>(&a, &b, 1, 1, p, q.num_sms, st);
-    case MM_S64: return mm_launch<false, 64, false, true, MM_DGATE>(&a, &b, 1, 1, p, q.num_sms, st);
-    default: return -1;
-  }
+  return mm_launch<false, true, MM_DGATE>(&a, &b, 1, 1, p, q.num_sms, st);
 }
 
 int launch_gated_dx(const GatedBackwardParams& q, cudaStream_t st) {
@@ -788,12 +1068,7 @@ int launch_gated_dx(const GatedBackwardParams& q, cudaStream_t st) {
   p.ldy[0] = q.ld_dx;
   const MmOperand a[2] = {{q.dg, q.M, q.F, q.F}, {q.du, q.M, q.F, q.F}};
   const MmOperand b[2] = {{q.gate, q.F, q.H, q.H}, {q.up, q.F, q.H, q.H}};
-  switch (mm_shape(p, 1, q.num_sms, MM_S64)) {
-    case MM_PAIR256: return mm_launch<true, 256, false, true, MM_LINEAR>(a, b, 2, 2, p, q.num_sms, st);
-    case MM_S128: return mm_launch<false, 128, false, true, MM_LINEAR>(a, b, 2, 2, p, q.num_sms, st);
-    case MM_S64: return mm_launch<false, 64, false, true, MM_LINEAR>(a, b, 2, 2, p, q.num_sms, st);
-    default: return -1;
-  }
+  return mm_launch<false, true, MM_LINEAR>(a, b, 2, 2, p, q.num_sms, st);
 }
 
 int launch_gated_dw(const GatedBackwardParams& q, cudaStream_t st) {
@@ -817,11 +1092,7 @@ int launch_gated_dw(const GatedBackwardParams& q, cudaStream_t st) {
   add({q.dy, q.M, q.H, q.ld_dy}, {q.h, q.M, q.F, q.F}, q.ddown);
   if (n == 0) return 0;
   p.n_prob = n;
-  switch (mm_shape(p, 1, q.num_sms, MM_S128)) {
-    case MM_PAIR256: return mm_launch<true, 256, true, true, MM_LINEAR>(a, b, n, n, p, q.num_sms, st);
-    case MM_S128: return mm_launch<false, 128, true, true, MM_LINEAR>(a, b, n, n, p, q.num_sms, st);
-    default: return -1;
-  }
+  return mm_launch<true, true, MM_LINEAR>(a, b, n, n, p, q.num_sms, st);
 }
 
 }  // namespace qi
