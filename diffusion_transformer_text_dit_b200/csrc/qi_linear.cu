@@ -18,7 +18,7 @@
 // and MMA issuer, warps 2..9 epilogue (warp w reads TMEM lanes 32 (w % 4) .. +
 // 31; two warps share a lane quarter).  Large products run on persistent CTA
 // pairs with 256 x 256 tiles (mm_kernel), middle ones on 128 x 128 tiles whose
-// K a cluster shares (mm_split_kernel), up to 16 rows of A on warp-level MMAs
+// K a cluster shares (mm_split_kernel), up to 32 rows of A on warp-level MMAs
 // that stream the weights (skinny_kernel).  MM_GATE takes half of the B rows
 // from each weight, so a tile holds gate columns next to the same up columns
 // and their product never leaves the registers; in a pair, each CTA loads one
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(MM_THREADS, PAIR ? 1 : 2)
 
 // ---------------------------------------------------------------- few rows
 //
-// M <= 16 rows: the product is bound by reading the weights once, so the
+// M <= 32 rows: the product is bound by reading the weights once, so the
 // weights go straight from memory into the fragments of warp-level MMAs
 // (m16n8k16: 16 weight rows against 8 rows of a), with no staging and no
 // 128-row tile that would be almost empty.  A thread's fragment of a 32-wide
@@ -714,7 +714,6 @@ __device__ __forceinline__ uint4 ld_stream16(const uint16_t* p) {
 template <int NT, bool GATE>
 __global__ void __launch_bounds__(SK_THREADS, 2) skinny_kernel(const SkinnyParams p) {
   constexpr int MATS = GATE ? 2 : 1;
-  constexpr int U = GATE ? 1 : 2;   // 64-wide pieces of K per batch of loads: 8 loads of weights
   constexpr int STEP = SK_THREADS / 32 * 64;
   __shared__ float red[SK_THREADS / 32][MATS][NT * 8][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -741,37 +740,33 @@ __global__ void __launch_bounds__(SK_THREADS, 2) skinny_kernel(const SkinnyParam
   for (int j = 0; j < NT; ++j) ar[j] = p.a + static_cast<size_t>(min(8 * j + g, p.M - 1)) * p.lda;
   // two batches of loads in turn: one is on its way while the other is multiplied
   struct Batch {
-    uint4 w[U][2][MATS][2], x[U][2][NT];
+    uint4 w[2][MATS][2], x[2][NT];   // of a 64-wide piece of K
   };
   auto load = [&](Batch& q, int kb) {
 #pragma unroll
-    for (int b = 0; b < U; ++b)
+    for (int sub = 0; sub < 2; ++sub) {
+      const int k = kb + 32 * sub + 8 * t;   // K % 8 == 0: a chunk of 8 lies inside or outside
+      const bool in = k < p.K;
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {
-        const int k = kb + b * STEP + 32 * sub + 8 * t;   // K % 8 == 0: a chunk of 8 lies inside or outside
-        const bool in = k < p.K;
+      for (int i = 0; i < MATS; ++i)
 #pragma unroll
-        for (int i = 0; i < MATS; ++i)
+        for (int e = 0; e < 2; ++e) q.w[sub][i][e] = in ? ld_stream16(wr[i][e] + k) : zero;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) q.w[b][sub][i][e] = in ? ld_stream16(wr[i][e] + k) : zero;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          q.x[b][sub][j] = in && 8 * j + g < p.M ? *reinterpret_cast<const uint4*>(ar[j] + k) : zero;
-      }
+      for (int j = 0; j < NT; ++j)
+        q.x[sub][j] = in && 8 * j + g < p.M ? *reinterpret_cast<const uint4*>(ar[j] + k) : zero;
+    }
   };
   auto multiply = [&](const Batch& q) {
 #pragma unroll
-    for (int b = 0; b < U; ++b)
+    for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub)
+      for (int i = 0; i < MATS; ++i)
 #pragma unroll
-        for (int i = 0; i < MATS; ++i)
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const uint4 w0 = q.w[b][sub][i][0], w1 = q.w[b][sub][i][1], x = q.x[b][sub][j];
-            mma_16816(acc[i][j], w0.x, w1.x, w0.y, w1.y, x.x, x.y);
-            mma_16816(acc[i][j], w0.z, w1.z, w0.w, w1.w, x.z, x.w);
-          }
+        for (int j = 0; j < NT; ++j) {
+          const uint4 w0 = q.w[sub][i][0], w1 = q.w[sub][i][1], x = q.x[sub][j];
+          mma_16816(acc[i][j], w0.x, w1.x, w0.y, w1.y, x.x, x.y);
+          mma_16816(acc[i][j], w0.z, w1.z, w0.w, w1.w, x.z, x.w);
+        }
   };
   pdl_wait();
   pdl_trigger();
@@ -780,10 +775,10 @@ __global__ void __launch_bounds__(SK_THREADS, 2) skinny_kernel(const SkinnyParam
     int kb = warp * 64;
     load(q0, kb);
 #pragma unroll 1
-    for (; kb < p.K; kb += 2 * U * STEP) {
-      load(q1, kb + U * STEP);
+    for (; kb < p.K; kb += 2 * STEP) {
+      load(q1, kb + STEP);
       multiply(q0);
-      load(q0, kb + 2 * U * STEP);
+      load(q0, kb + 2 * STEP);
       multiply(q1);
     }
   }
@@ -986,13 +981,20 @@ static int mm_launch(const MmOperand* A, const MmOperand* B, int n_ops_a, int n_
   return launch_result();
 }
 
-constexpr int SK_MAX_ROWS = 16;
+// 32 rows: against the 128-row tiles with K split over a cluster, 4096 x 4096
+// takes 9.8 us (tiles 12.7) at 20 rows and 12.2 (12.9) at 32; 4096 x 11008
+// 19.3 (23.2) and 25.2 (23.6); the gated pair of 4096 x 11008 41 (50) and 50
+// (51); 1024 x 1024 3.0 (5.6) and 3.1 (5.9).  With more rows the reads of a,
+// which every CTA makes from L2, cost more than the empty half of a tile.
+constexpr int SK_MAX_ROWS = 32;
 
 template <bool GATE>
 static int launch_skinny(const SkinnyParams& s, cudaStream_t st) {
   const dim3 grid((s.N + 15) / 16);
   if (s.M <= 8) launch_pdl(skinny_kernel<1, GATE>, grid, dim3(SK_THREADS), 0, st, 1, s);
-  else launch_pdl(skinny_kernel<2, GATE>, grid, dim3(SK_THREADS), 0, st, 1, s);
+  else if (s.M <= 16) launch_pdl(skinny_kernel<2, GATE>, grid, dim3(SK_THREADS), 0, st, 1, s);
+  else if (s.M <= 24) launch_pdl(skinny_kernel<3, GATE>, grid, dim3(SK_THREADS), 0, st, 1, s);
+  else launch_pdl(skinny_kernel<4, GATE>, grid, dim3(SK_THREADS), 0, st, 1, s);
   return launch_result();
 }
 

@@ -149,6 +149,19 @@ def test_attention_many_sequences_share_keys(ctx):
                rand(400, kvh * 128, seed=2), table(rows), heads, kvh)
 
 
+@pytest.mark.parametrize("heads,kvh", [(8, 2), (3, 1), (32, 1), (40, 1), (96, 1)])
+def test_attention_short_sequences_beside_long_ones(ctx, heads, kvh):
+    """Single tokens, some behind a few keys and some behind thousands, in one table
+    with prompts: more units of work than an ordered list holds, and fewer."""
+    for tokens in (6, qi.QI_MAX_SEQS - 4):
+        ql = [1] * tokens + [700, 128, 33, 0]
+        kl = [1 + (i * 97) % 400 for i in range(tokens - 3)] + [2048, 2049, 5000, 700, 900, 33, 0]
+        spans, nq, nk = packed(ql, kl)
+        got = check_attn(ctx, rand(nq, heads * 128), rand(nk, kvh * 128, seed=1), rand(nk, kvh * 128, seed=2),
+                         spans, heads, kvh)
+        assert got.shape == (nq, heads * 128)
+
+
 def test_attention_fused_rows_and_strides(ctx):
     """q, k, v as column ranges of one fused block, o into a wider padded buffer:
     the columns and rows around the result stay as they were."""
@@ -334,6 +347,16 @@ def test_linear_shapes(ctx, M, n, k):
     check_linear(ctx, a, w, b, qi.QI_ACT_GELU_TANH, rand(M, n, seed=4))
 
 
+@pytest.mark.parametrize("M", [20, 24, 25, 31, 32, 33, 95])
+@pytest.mark.parametrize("n,k", [(8, 8), (24, 72), (200, 128), (256, 192), (520, 4096), (2000, 520)])
+def test_linear_few_rows(ctx, M, n, k):
+    """Around the last row count that streams the weights, and middle sizes whose K is
+    shared by several CTAs: fewer pieces of K than CTAs, unequal shares."""
+    a, w, b = rand(M, k), rand(n, k, seed=1, scale=0.05), rand(n, seed=2)
+    check_linear(ctx, a, w, b, qi.QI_ACT_SILU, rand(M, n, seed=3))
+    check_linear(ctx, a, w, None, qi.QI_ACT_NONE)
+
+
 @pytest.mark.parametrize("M", [1, 5, 40, 260])
 @pytest.mark.parametrize("n", [1, 3, 33, 255, 257])
 def test_linear_odd_outputs(ctx, M, n):
@@ -440,7 +463,7 @@ def check_backward(ctx, w, x, wg, wu, wd, act, gu, dy):
     return dict(zip(refs, got))
 
 
-SHAPES = [(1, 64, 128), (16, 200, 72), (17, 256, 520), (100, 512, 1384), (333, 1024, 2816), (129, 8, 8),
+SHAPES = [(1, 64, 128), (16, 200, 72), (25, 136, 328), (32, 520, 200), (33, 64, 4096), (40, 4096, 64), (17, 256, 520), (100, 512, 1384), (333, 1024, 2816), (129, 8, 8),
           (700, 1032, 264)]
 
 
