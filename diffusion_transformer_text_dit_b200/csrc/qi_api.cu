@@ -207,7 +207,8 @@ bool make_tmap_rows3(CUtensorMap* map, const void* base, uint64_t inner, uint64_
   cuuint32_t box[3] = {box_inner, box_mid, box_rows};
   cuuint32_t estr[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                box_inner * 2 > 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -59,7 +59,8 @@ constexpr int AP_ROWS = 128;
 constexpr int AP_THREADS = 192;   // 4 softmax warps, TMA, MMA
 constexpr int AP_TILE = 128 * 128 * 2;
 constexpr int AP_HALF = 128 * 128;
-constexpr int AP_SMEM = 1024 + 3 * AP_TILE + 128;   // Q, K, V
+constexpr int AP_OUT = 32 * 64;   // bytes of a softmax warp's staged output: 32 rows x 32 columns
+constexpr int AP_SMEM = 3 * AP_TILE + 8 * AP_OUT + 128;   // Q, K, V, two stages per warp
 static_assert(2 * (AP_SMEM + 1024) <= 233472, "two CTAs per SM");
 
 struct ApKernelParams {
@@ -68,6 +69,7 @@ struct ApKernelParams {
   int ldq;
   uint16_t* o;
   int ldo, kv_heads;
+  int tma_out;       // tile kernel: the output map's box holds 32 rows of a tile
   int row_blocks;    // token kernel: 16-row blocks per unit
   float sm_scale;
   float* part_o;     // [slots][slot_rows][128]
@@ -128,6 +130,19 @@ __device__ __forceinline__ void tma_load_3d_elect(const CUtensorMap* map, uint32
       " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(smem_u32(smem)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// Tiled bulk store of a box, in the current bulk group, and the wait until at
+// most N groups still read shared memory.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(smem)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_group_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 // Ask for a tile in L2.
@@ -245,16 +260,20 @@ static_assert(AP_MAX_SEQS <= 256, "sequence in 8 bits");
 
 __global__ void __launch_bounds__(AP_THREADS, 2)
     ap_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ ApKernelParams p) {
+              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+              const __grid_constant__ ApKernelParams p) {
   const PackedPlan& d = p.plan;
   int* status = p.status;
-  extern __shared__ uint8_t ap_smem_raw[];
-  const uint32_t raw_addr = smem_u32(ap_smem_raw);
-  uint8_t* smem = ap_smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {   // (two CTAs leave no room to align it by hand)
+    if (threadIdx.x == 0) set_error(status, QI_DEV_ERR_BOUNDS);
+    return;
+  }
   uint8_t* sQ = smem;
   uint8_t* sK = smem + AP_TILE;
   uint8_t* sV = smem + 2 * AP_TILE;
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + 3 * AP_TILE);
+  uint8_t* sO = smem + 3 * AP_TILE;   // [4 warps][2][AP_OUT]
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(sO + 8 * AP_OUT);
   uint64_t* k_full = q_full + 1;
   uint64_t* v_full = q_full + 2;
   uint64_t* s_full = q_full + 3;   // S of a tile and P V of the tile before complete
@@ -278,6 +297,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
+    prefetch_tmap(&tmO);
   }
   if (warp == 5) {
     tmem_alloc(tmem_slot, 256);
@@ -539,9 +559,10 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       if (!ok) break;
       if (w.n > 0 && !mbar_wait_warp(o_full, units & 1, status)) { ok = false; break; }
       tc_fence_after();
-      // where this row goes: fp32 partial of the key range, or the output (a thread writes its own
-      // row: staging rows through shared memory for wider segments takes several times the
-      // load/store instructions, which queue behind the other CTA's exponentials)
+      // where this row goes: fp32 partial of the key range, or the output.  32 whole rows leave
+      // through TMA, 32 columns at a time (a warp's own stores, 32 rows of 16 bytes each, keep the
+      // load/store unit busy for 2000 clocks per tile); a cut tile, or a G that does not divide 32,
+      // is stored row by row.
       const bool split = sq.nsp > 1;
       const float inv = l > 0.f ? __fdividef(1.0f, l) : 0.f;
       const uint64_t inv2 = f2_pack(inv, inv);
@@ -550,29 +571,45 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
                               : static_cast<size_t>(sq.q0 + pos) * p.ldo + (w.u.h * G + row_head) * 128;
       if (split && live) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m_ref, l);
       if (warp_live && (w.n > 0 || !split)) {   // (a range without a key has weight 0, whatever its O)
+        const bool whole = !split && p.tma_out && __all_sync(0xffffffffu, live);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t r[32];
           if (w.n > 0) tmem_ld32(tO + 32 * c, r);
-          if (!live) continue;
           if (split) {
+            if (!live) continue;
             float4* dst = reinterpret_cast<float4*>(p.part_o + at * 128 + c * 32);
 #pragma unroll
             for (int v = 0; v < 8; ++v)
               dst[v] = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
                                    __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(p.o + at + c * 32);
+            continue;
+          }
+          uint8_t* mine = sO + (warp * 2 + (c & 1)) * AP_OUT;
+          if (whole) {   // the stage's last store has read it
+            if (lane == 0) bulk_wait_group_read<1>();
+            __syncwarp();
+          }
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              uint32_t y[4];
+          for (int v = 0; v < 4; ++v) {
+            uint32_t y[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float a, b;
-                f2_unpack(f2_mul(f2_pack(__uint_as_float(r[8 * v + 2 * e]), __uint_as_float(r[8 * v + 2 * e + 1])), inv2), a, b);
-                y[e] = lim == 0 ? 0u : pack_bf16x2(a, b);   // a row that sees no key: 0
-              }
-              dst[v] = make_uint4(y[0], y[1], y[2], y[3]);
+            for (int e = 0; e < 4; ++e) {
+              float a, b;
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(r[8 * v + 2 * e]), __uint_as_float(r[8 * v + 2 * e + 1])), inv2), a, b);
+              y[e] = lim == 0 ? 0u : pack_bf16x2(a, b);   // a row that sees no key: 0
+            }
+            const uint4 x = make_uint4(y[0], y[1], y[2], y[3]);
+            // (the 64-byte swizzle: chunk v of row i at chunk v ^ (i / 2 mod 4))
+            if (whole) *reinterpret_cast<uint4*>(mine + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4)) = x;
+            else if (live) *reinterpret_cast<uint4*>(p.o + at + c * 32 + v * 8) = x;
+          }
+          if (whole) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&tmO, mine, 32 * c, w.u.h * G + (warp * 32) % G, sq.q0 + w.u.ct * P + warp * 32 / G);
+              bulk_commit_group();
             }
           }
         }
@@ -583,6 +620,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     }
   }
 
+  if (warp < 4 && lane == 0) bulk_wait_group_read<0>();   // the staged rows are read before the CTA leaves
   tc_fence_before();
   __syncthreads();
   if (warp == 5) {
@@ -1139,8 +1177,16 @@ int launch_attention_packed(const PackedAttnParams& a, const PackedPlan& tile, c
     if (!make_tmap_rows3(&tq, a.q, 128, a.heads, a.q_rows, static_cast<uint64_t>(a.ldq) * 2, 64, tile.G, tile.P) ||
         !kv_maps(&tk, &tv, AP_ROWS))
       return -2;
+    // output boxes: the 32 rows of a softmax warp, min(G, 32) heads x 32 / G positions
+    CUtensorMap to;
+    p.tma_out = 32 % tile.G == 0 || tile.G % 32 == 0;
+    const uint32_t box_heads = tile.G < 32 ? tile.G : 32;
+    if (!p.tma_out) to = tq;
+    else if (!make_tmap_rows3(&to, a.o, 128, a.heads, a.q_rows, static_cast<uint64_t>(a.ldo) * 2, 32, box_heads,
+                              32 / box_heads))
+      return -2;
     partials(tile, 0);
-    launch_pdl(ap_kernel, dim3(std::min(tile.units, 2 * a.num_sms)), dim3(AP_THREADS), AP_SMEM, st, 1, tq, tk, tv, p);
+    launch_pdl(ap_kernel, dim3(std::min(tile.units, 2 * a.num_sms)), dim3(AP_THREADS), AP_SMEM, st, 1, tq, tk, tv, to, p);
     if (launch_result() || launch_join(p, st)) return -1;
   }
   if (token.units > 0) {

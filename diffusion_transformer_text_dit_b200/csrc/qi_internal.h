@@ -128,7 +128,8 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, ui
                   uint32_t box_outer, bool swizzle128 = true);
 
 // TMA descriptor for bf16 rows [rows][mid][inner] (mid contiguous pieces of
-// `inner` values per row), box box_inner x box_mid x box_rows, 128-byte swizzle.
+// `inner` values per row), box box_inner x box_mid x box_rows, box rows (of
+// 64 or 32 values) swizzled over 128 or 64 bytes.
 bool make_tmap_rows3(CUtensorMap* map, const void* base, uint64_t inner, uint64_t mid, uint64_t rows,
                      uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_mid,
                      uint32_t box_rows);
