@@ -203,7 +203,7 @@ bool make_tmap_rows3(CUtensorMap* map, const void* base, uint64_t inner, uint64_
   const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
   if (!encode) return false;
   cuuint64_t dims[3] = {inner, mid, rows};
-  cuuint64_t strides[2] = {inner * 2, row_stride_bytes};
+  cuuint64_t strides[2] = {mid > 1 ? inner * 2 : row_stride_bytes, row_stride_bytes};
   cuuint32_t box[3] = {box_inner, box_mid, box_rows};
   cuuint32_t estr[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,

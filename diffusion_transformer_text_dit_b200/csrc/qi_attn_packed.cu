@@ -120,31 +120,6 @@ __host__ __device__ __forceinline__ int ap_slot(const PackedPlan& d, int kv_head
   return d.seq[s].sbase + (ct * d.seq[s].nsp + j) * kv_heads + h;
 }
 
-// tma_load_2d_elect with three coordinates.
-__device__ __forceinline__ void tma_load_3d_elect(const CUtensorMap* map, uint32_t bar, void* smem, int x, int y,
-                                                  int z) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(smem_u32(smem)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
-// Tiled bulk store of a box, in the current bulk group, and the wait until at
-// most N groups still read shared memory.
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(smem_u32(smem)), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-template <int N>
-__device__ __forceinline__ void bulk_wait_group_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-
 // Ask for a tile in L2.
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(

@@ -41,6 +41,9 @@ constexpr int MM_MAX_PROB = 3;
 
 struct MmMaps {
   CUtensorMap a[MM_MAX_PROB], b[MM_MAX_PROB];
+  // persistent kernel, boxes of 32 rows x 32 columns: the outputs (MM_DGATE: dg,
+  // du, h) and the residual or gate | up
+  CUtensorMap y[MM_MAX_PROB], x;
 };
 
 struct MmParams {
@@ -50,7 +53,7 @@ struct MmParams {
   int tiles_end[MM_MAX_PROB];  // running number of tiles
   int group_m[MM_MAX_PROB];    // tile order (tile_coords)
   int segs;                    // 2: operands a[0], b[0], then a[1], b[1], into one sum
-  uint16_t* y[MM_MAX_PROB];
+  uint16_t* y[MM_MAX_PROB];    // MM_DGATE: dg, du and, unless null, h, each [M, F]
   int ldy[MM_MAX_PROB];
   int vec;                     // rows of y and res may be accessed 16 bytes at a time
   const uint16_t* bias;
@@ -58,17 +61,15 @@ struct MmParams {
   int ld_res;
   int act;
   uint16_t* gu;                // MM_GATE: optional output, MM_DGATE: input, [M, 2F]
-  uint16_t* dg;                // MM_DGATE outputs [M, F]
-  uint16_t* du;
-  uint16_t* h;
   int* status;
 };
 
 constexpr int MM_TILE = 128 * 128;   // bytes of a stage's A or B tile of one CTA: 128 x 64 bf16
 constexpr int MM_BN = 256;           // persistent kernel: columns of a pair's tile
 constexpr int MM_STAGES = 6;
-constexpr int MM_SMEM = 1024 + MM_STAGES * 2 * MM_TILE + 256;
-static_assert(2 * MM_STAGES + 6 <= 32, "barrier area");
+constexpr int MM_OUT = 32 * 64;      // bytes of an epilogue warp's stage: 32 rows x 32 bf16 columns
+constexpr int MM_SMEM = 1024 + MM_STAGES * 2 * MM_TILE + MM_EPI_WARPS * 2 * MM_OUT + 256;
+static_assert(2 * MM_STAGES + 6 + MM_EPI_WARPS <= 32, "barrier area");
 static_assert(MM_SMEM <= 232448, "shared memory per CTA");
 
 // ---------------------------------------------------------------- activations
@@ -143,18 +144,18 @@ __device__ __forceinline__ void mm_tempty_signal(uint32_t addr) {
 
 // ---------------------------------------------------------------- epilogue
 
-// Output columns nb .. nb + 7 of row m from their fp32 sums v (and, for
-// MM_GATE, the up projection's u): the fused operation and the store.
+// 8 output columns from their fp32 sums v (MM_GATE: and the up projection's u)
+// and inputs: the fused operation, rounded once per output.
+//   MM_LINEAR  x0 residual (with p.res); o0 = act(v + bias) + x0
+//   MM_GATE    o0 = act(v) u, o1 = v, o2 = u
+//   MM_DGATE   x0 gate, x1 up; o0 = dgate, o1 = dup, o2 = act(gate) up
 template <int EPI>
-__device__ __forceinline__ void mm_out8(const MmParams& p, int pr, int m, int nb, float (&v)[8],
-                                        const float (&u)[8]) {
-  const int N = p.N[pr], ncols = N - nb;
-  if (ncols <= 0) return;
-  uint32_t pk[4];
+__device__ __forceinline__ void mm_math8(const MmParams& p, float (&v)[8], const float (&u)[8], int nb, int ncols,
+                                         const uint32_t (&x0)[4], const uint32_t (&x1)[4], uint32_t (&o0)[4],
+                                         uint32_t (&o1)[4], uint32_t (&o2)[4]) {
   if constexpr (EPI == MM_LINEAR) {
-    const bool vec = p.vec != 0;
-    uint32_t b[4];
     if (p.bias) {
+      uint32_t b[4];
       load8(p.bias + nb, b, ncols, true);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -170,64 +171,113 @@ __device__ __forceinline__ void mm_out8(const MmParams& p, int pr, int m, int nb
       for (int i = 0; i < 8; ++i) v[i] = act_f(v[i], ACT_GELU_TANH);
     }
     if (p.res) {
-      load8(p.res + static_cast<size_t>(m) * p.ld_res + nb, b, ncols, vec);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[2 * i] += bf16_lo(b[i]);
-        v[2 * i + 1] += bf16_hi(b[i]);
+        v[2 * i] += bf16_lo(x0[i]);
+        v[2 * i + 1] += bf16_hi(x0[i]);
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pk[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-    store8(p.y[pr] + static_cast<size_t>(m) * p.ldy[pr] + nb, pk, ncols, vec);
+    for (int i = 0; i < 4; ++i) o0[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
   } else if constexpr (EPI == MM_GATE) {
-    // the activation and the product in fp32, rounded once (F % 8 == 0: whole 16-byte groups)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      pk[i] = pack_bf16x2(act_f(v[2 * i], p.act) * u[2 * i], act_f(v[2 * i + 1], p.act) * u[2 * i + 1]);
-    store8(p.y[0] + static_cast<size_t>(m) * N + nb, pk, ncols, true);
-    if (p.gu) {
-      uint16_t* row = p.gu + static_cast<size_t>(m) * 2 * N + nb;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) pk[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-      store8(row, pk, ncols, true);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) pk[i] = pack_bf16x2(u[2 * i], u[2 * i + 1]);
-      store8(row + N, pk, ncols, true);
-    }
-  } else {
-    uint32_t gg[4], uu[4];
-    const uint16_t* row = p.gu + static_cast<size_t>(m) * 2 * N + nb;
-    load8(row, gg, ncols, true);
-    load8(row + N, uu, ncols, true);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float u0 = bf16_lo(uu[i]), u1 = bf16_hi(uu[i]);
-      float a0, a1, e0, e1;
-      act_grad_f(bf16_lo(gg[i]), p.act, a0, e0);
-      act_grad_f(bf16_hi(gg[i]), p.act, a1, e1);
-      pk[i] = pack_bf16x2(a0 * u0, a1 * u1);
-      gg[i] = pack_bf16x2(v[2 * i] * u0 * e0, v[2 * i + 1] * u1 * e1);
-      uu[i] = pack_bf16x2(v[2 * i] * a0, v[2 * i + 1] * a1);
+      o0[i] = pack_bf16x2(act_f(v[2 * i], p.act) * u[2 * i], act_f(v[2 * i + 1], p.act) * u[2 * i + 1]);
+      o1[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      o2[i] = pack_bf16x2(u[2 * i], u[2 * i + 1]);
     }
-    const size_t at = static_cast<size_t>(m) * N + nb;
-    store8(p.dg + at, gg, ncols, true);
-    store8(p.du + at, uu, ncols, true);
-    if (p.h) store8(p.h + at, pk, ncols, true);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float u0 = bf16_lo(x1[i]), u1 = bf16_hi(x1[i]);
+      float a0, a1, e0, e1;
+      act_grad_f(bf16_lo(x0[i]), p.act, a0, e0);
+      act_grad_f(bf16_hi(x0[i]), p.act, a1, e1);
+      o0[i] = pack_bf16x2(v[2 * i] * u0 * e0, v[2 * i + 1] * u1 * e1);
+      o1[i] = pack_bf16x2(v[2 * i] * a0, v[2 * i + 1] * a1);
+      o2[i] = pack_bf16x2(a0 * u0, a1 * u1);
+    }
   }
+}
+
+// The same with the thread's own loads and stores: output columns nb .. nb + 7
+// of row m.  (Of the gated forms F % 8 == 0: whole 16-byte groups.)
+template <int EPI>
+__device__ __forceinline__ void mm_out8(const MmParams& p, int pr, int m, int nb, float (&v)[8],
+                                        const float (&u)[8]) {
+  const int N = p.N[pr], ncols = N - nb;
+  if (ncols <= 0) return;
+  const bool vec = p.vec != 0;
+  uint32_t x0[4] = {}, x1[4] = {}, o0[4], o1[4], o2[4];
+  uint16_t* row = EPI == MM_LINEAR ? nullptr : p.gu + static_cast<size_t>(m) * 2 * N + nb;
+  if (EPI == MM_LINEAR && p.res) load8(p.res + static_cast<size_t>(m) * p.ld_res + nb, x0, ncols, vec);
+  if (EPI == MM_DGATE) {
+    load8(row, x0, ncols, true);
+    load8(row + N, x1, ncols, true);
+  }
+  mm_math8<EPI>(p, v, u, nb, ncols, x0, x1, o0, o1, o2);
+  store8(p.y[pr] + static_cast<size_t>(m) * p.ldy[pr] + nb, o0, ncols, vec);
+  if (EPI == MM_GATE && p.gu) {
+    store8(row, o1, ncols, true);
+    store8(row + N, o2, ncols, true);
+  }
+  if (EPI == MM_DGATE) {
+    store8(p.y[1] + static_cast<size_t>(m) * N + nb, o1, ncols, true);
+    if (p.y[2]) store8(p.y[2] + static_cast<size_t>(m) * N + nb, o2, ncols, true);
+  }
+}
+
+// An epilogue warp's two stages and the barrier of its loads.
+struct MmStage {
+  uint8_t* buf;
+  uint64_t* bar;
+  uint32_t phase;
+  int turn;        // MM_LINEAR: chunks done, its parity is the stage
+  __device__ uint8_t* at(int i) const { return buf + (i & 1) * MM_OUT; }
+};
+
+// Inputs of the 32 x 32 chunk at (row, col) into the stages, once the stores
+// that read them are done.
+template <int EPI>
+__device__ __forceinline__ void mm_fetch(const MmMaps& maps, MmStage& s, int row, int col, int lane) {
+  if (lane == 0) bulk_wait_group_read<EPI == MM_DGATE ? 0 : 1>();
+  __syncwarp();
+  const uint32_t bar = smem_u32(s.bar);
+  mbar_expect_elect(s.bar, EPI == MM_DGATE ? 2 * MM_OUT : MM_OUT);
+  tma_load_3d_elect(&maps.x, bar, s.at(EPI == MM_DGATE ? 0 : s.turn), col, 0, row);
+  if (EPI == MM_DGATE) tma_load_3d_elect(&maps.x, bar, s.at(1), col, 1, row);
 }
 
 // One accumulator tile of the persistent kernel: rows m0 .. m0 + 127 of this
 // CTA, output columns from n0.  Signals the accumulator buffer free after this
-// warp's last TMEM read.
+// warp's last TMEM read.  A thread holds one row, so its own accesses would be
+// 16 bytes in each of 32 rows, 32 passes of the load/store unit each; instead a
+// warp's 32 x 32 chunk goes through shared memory and TMA brings the inputs and
+// takes the outputs (TMA keeps to the rows and columns that exist).  Rows that
+// are not 16-byte aligned (p.vec == 0) are accessed directly.
+// The 64-byte swizzle of a stage: 16-byte group q of row r at q ^ (r / 2 mod 4).
 template <int EPI>
-__device__ __forceinline__ void mm_epilogue(const MmParams& p, int pr, uint32_t tacc, int m0, int n0,
-                                            int quarter, int half, int lane, uint32_t tempty_addr) {
+__device__ __forceinline__ bool mm_epilogue(const MmMaps& maps, const MmParams& p, int pr, uint64_t* tfull,
+                                            uint32_t tfull_phase, uint32_t tacc, int m0, int n0, int quarter,
+                                            int half, int lane, uint32_t tempty_addr, MmStage& s) {
   constexpr int W = EPI == MM_GATE ? MM_BN / 2 : MM_BN;   // output columns of a tile
   constexpr int CH = W / 32;
-  const int m = m0 + quarter * 32 + lane;
-  const bool row_ok = m < p.M[pr];
+  const int row0 = m0 + quarter * 32, m = row0 + lane, N = p.N[pr];
+  const bool vec = EPI != MM_LINEAR || p.vec;
+  const bool rows_in = row0 < p.M[pr];
+  const bool has_in = EPI == MM_DGATE || (EPI == MM_LINEAR && p.res && vec);
   const uint32_t t_row = tacc + (static_cast<uint32_t>(quarter * 32) << 16);
+  bool fetched = has_in && rows_in && n0 + half * 32 < N;
+  if (fetched) mm_fetch<EPI>(maps, s, row0, n0 + half * 32, lane);
+  if (!mbar_wait_warp(tfull, tfull_phase, p.status)) {
+    if (fetched) {   // the load lands before the CTA exits (bounded)
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(s.bar, s.phase) && globaltimer_ns() - t0 < QI_WAIT_NS) {
+      }
+    }
+    return false;
+  }
+  tc_fence_after();
 #pragma unroll 1
   for (int c = half; c < CH; c += 2) {
     __syncwarp();
@@ -240,18 +290,109 @@ __device__ __forceinline__ void mm_epilogue(const MmParams& p, int pr, uint32_t 
       __syncwarp();
       if (lane == 0) mm_tempty_signal(tempty_addr);
     }
-    if (!row_ok) continue;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float v[8], u[8];
+    const int col0 = n0 + c * 32;
+    if (!rows_in || col0 >= N) continue;
+    float v[8], u[8];
+    auto sums = [&](int q) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         v[i] = __uint_as_float(r[8 * q + i]);
         u[i] = EPI == MM_GATE ? __uint_as_float(r2[8 * q + i]) : 0.f;
       }
-      mm_out8<EPI>(p, pr, m, n0 + c * 32 + q * 8, v, u);
+    };
+    if (!vec) {
+      if (m < p.M[pr])
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          sums(q);
+          mm_out8<EPI>(p, pr, m, col0 + q * 8, v, u);
+        }
+      continue;
     }
+    if (has_in) {
+      if (!mbar_wait_warp(s.bar, s.phase, p.status)) return false;
+      s.phase ^= 1u;
+    } else {
+      if (lane == 0) bulk_wait_group_read<1>();   // the stage's last store has read it
+      __syncwarp();
+    }
+    auto group = [&](uint8_t* stage, int q) {
+      return reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
+    };
+    auto put = [&](uint8_t* stage, int q, const uint32_t (&o)[4]) {
+      *group(stage, q) = make_uint4(o[0], o[1], o[2], o[3]);
+    };
+    auto send = [&](const CUtensorMap* map, const uint8_t* stage, int which) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(map, stage, col0, which, row0);
+        bulk_commit_group();
+      }
+    };
+    auto reuse = [&] {   // the stage of the store before the last one
+      if (lane == 0) bulk_wait_group_read<1>();
+      __syncwarp();
+    };
+    uint8_t* s0 = s.at(EPI == MM_DGATE ? 0 : s.turn);
+    uint8_t* s1 = s.at(EPI == MM_DGATE ? 1 : s.turn + 1);
+    uint32_t o0[4], o1[4], o2[EPI == MM_DGATE ? 4 : 1][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t x0[4] = {}, x1[4] = {};
+      if (has_in) {
+        const uint4 x = *group(s0, q);
+        x0[0] = x.x; x0[1] = x.y; x0[2] = x.z; x0[3] = x.w;
+      }
+      if (EPI == MM_DGATE) {
+        const uint4 x = *group(s1, q);
+        x1[0] = x.x; x1[1] = x.y; x1[2] = x.z; x1[3] = x.w;
+      }
+      sums(q);
+      mm_math8<EPI>(p, v, u, col0 + q * 8, N - col0 - q * 8, x0, x1, o0, o1, o2[EPI == MM_DGATE ? q : 0]);
+      put(s0, q, o0);
+      if (EPI == MM_DGATE) put(s1, q, o1);
+    }
+    if constexpr (EPI == MM_LINEAR) {
+      send(&maps.y[pr], s0, 0);
+      ++s.turn;
+    } else if constexpr (EPI == MM_GATE) {
+      send(&maps.y[0], s0, 0);
+      ++s.turn;
+      if (p.gu) {
+        reuse();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o1[i] = pack_bf16x2(__uint_as_float(r[8 * q + 2 * i]), __uint_as_float(r[8 * q + 2 * i + 1]));
+          put(s1, q, o1);
+        }
+        send(&maps.x, s1, 0);
+        reuse();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o1[i] = pack_bf16x2(__uint_as_float(r2[8 * q + 2 * i]), __uint_as_float(r2[8 * q + 2 * i + 1]));
+          put(s0, q, o1);
+        }
+        send(&maps.x, s0, 1);
+        s.turn += 2;
+      }
+    } else {
+      send(&maps.y[0], s0, 0);
+      send(&maps.y[1], s1, 0);
+      if (p.y[2]) {
+        reuse();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) put(s0, q, o2[q]);
+        send(&maps.y[2], s0, 0);
+      }
+    }
+    if (has_in && c + 2 < CH && col0 + 64 < N) mm_fetch<EPI>(maps, s, row0, col0 + 64, lane);
   }
+  return true;
 }
 
 // Product and tile coordinates of a tile number, for tiles of BM rows and W columns.
@@ -312,13 +453,15 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES * MM_TILE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * 2 * MM_TILE);
+  uint8_t* sOut = smem + STAGES * 2 * MM_TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + MM_EPI_WARPS * 2 * MM_OUT);
   uint64_t* full = bars;                     // [STAGES] (the even CTA's)
   uint64_t* empty = bars + STAGES;           // [STAGES]
   uint64_t* tfull = bars + 2 * STAGES;       // [2]
   uint64_t* tempty = bars + 2 * STAGES + 2;  // [2] (the even CTA's)
   uint64_t* drain = bars + 2 * STAGES + 4;   // MMA drain on the error path
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+  uint64_t* xfull = bars + 2 * STAGES + 5;   // [MM_EPI_WARPS] inputs of the epilogue
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xfull + MM_EPI_WARPS);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -336,6 +479,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
       mbar_init(&tempty[a], 2 * MM_EPI_WARPS);
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < MM_EPI_WARPS; ++i) mbar_init(&xfull[i], 1);
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -441,16 +585,18 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     const int half = (warp - 2) >> 2;
     int acc = 0;
     uint32_t acc_phase = 0;
+    MmStage stage{sOut + (warp - 2) * 2 * MM_OUT, &xfull[warp - 2], 0, 0};
     for (int tile = worker; tile < num_tiles; tile += workers) {
       int pr, mt, nt;
       mm_tile<256, W>(p, tile, pr, mt, nt);
-      if (!mbar_wait_warp(&tfull[acc], acc_phase, p.status)) break;
-      tc_fence_after();
-      mm_epilogue<EPI>(p, pr, tmem_base + static_cast<uint32_t>(acc * MM_BN), mt * 256 + rank * 128, nt * W,
-                       quarter, half, lane, mapa_shared(smem_u32(&tempty[acc]), 0));
+      if (!mm_epilogue<EPI>(maps, p, pr, &tfull[acc], acc_phase, tmem_base + static_cast<uint32_t>(acc * MM_BN),
+                            mt * 256 + rank * 128, nt * W, quarter, half, lane,
+                            mapa_shared(smem_u32(&tempty[acc]), 0), stage))
+        break;
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
+    if (lane == 0) bulk_wait_group_read<0>();   // the stages are read before the CTA leaves
   }
 
   // Neither CTA of a pair leaves (or frees TMEM) while the other may still read
@@ -639,38 +785,40 @@ __global__ void __launch_bounds__(MM_THREADS, PAIR ? 1 : 2)
     else tmem_dealloc(tmem_base, C::COLS);
   }
   if (warp >= 2 && ok) {
-    // columns [part W / S, + W / S) of this CTA's rows, half of them per thread
-    const int et = threadIdx.x - 64, row = et & 127, per = W / S / 2;
-    const int m = m0 + row, c0 = part * (W / S) + (et >> 7) * per;
-    const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(row) * 16;
-    if (m < p.M[pr])
+    // columns [part W / S, + W / S) of this CTA's rows, 8 of a row at a time; a
+    // warp takes 8 rows x 32 columns (16 x 16), so its accesses are whole sectors
+    const int ng = W / S / 8;
 #pragma unroll 1
-      for (int c = c0; c < c0 + per; c += 8) {
-        float v[8], u[8];
+    for (int item = threadIdx.x - 64; item < 128 * ng; item += 256) {
+      const int c = part * (W / S) + ((item >> 3) & (ng - 1)) * 8;
+      const int row = ((item >> 3) / ng) * 8 + (item & 7);
+      if (m0 + row >= p.M[pr]) continue;
+      const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(row) * 16;
+      float v[8], u[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.f;
-#pragma unroll 1
-        for (int s = 0; s < S; ++s) {
-          const uint32_t peer = static_cast<uint32_t>(PAIR ? 2 * s + rank : s);
-          const uint32_t from = (ctas > 1 ? mapa_shared(mine, peer) : mine) + (c >> 2) * 2048;
+      for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.f;
+#pragma unroll 2
+      for (int s = 0; s < S; ++s) {
+        const uint32_t peer = static_cast<uint32_t>(PAIR ? 2 * s + rank : s);
+        const uint32_t from = (ctas > 1 ? mapa_shared(mine, peer) : mine) + (c >> 2) * 2048;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float4 x = ld_cluster4(from + e * 2048);
-            v[4 * e] += x.x;
-            v[4 * e + 1] += x.y;
-            v[4 * e + 2] += x.z;
-            v[4 * e + 3] += x.w;
-            if (EPI == MM_GATE) {
-              const float4 y = ld_cluster4(from + (W / 4 + e) * 2048);   // the up columns, W further on
-              u[4 * e] += y.x;
-              u[4 * e + 1] += y.y;
-              u[4 * e + 2] += y.z;
-              u[4 * e + 3] += y.w;
-            }
+        for (int e = 0; e < 2; ++e) {
+          const float4 x = ld_cluster4(from + e * 2048);
+          v[4 * e] += x.x;
+          v[4 * e + 1] += x.y;
+          v[4 * e + 2] += x.z;
+          v[4 * e + 3] += x.w;
+          if (EPI == MM_GATE) {
+            const float4 y = ld_cluster4(from + (W / 4 + e) * 2048);   // the up columns, W further on
+            u[4 * e] += y.x;
+            u[4 * e + 1] += y.y;
+            u[4 * e + 2] += y.z;
+            u[4 * e + 3] += y.w;
           }
         }
-        mm_out8<EPI>(p, pr, m, nt * W + c, v, u);
       }
+      mm_out8<EPI>(p, pr, m0 + row, nt * W + c, v, u);
+    }
   }
   if (ctas > 1) cluster_sync_all();   // no CTA leaves while another may read its sums
 }
@@ -975,6 +1123,17 @@ static int mm_launch(const MmOperand* A, const MmOperand* B, int n_ops_a, int n_
     launch_result();
     return -1;
   }
+  auto out_map = [](CUtensorMap* m, const void* base, int cols, int mid, int rows, long ld) {
+    return make_tmap_rows3(m, base, cols, mid, rows, static_cast<uint64_t>(ld) * 2, 32, 1, 32);
+  };
+  bool ok = true;
+  for (int i = 0; i < (EPI == MM_DGATE ? 3 : p.n_prob) && p.vec; ++i) {
+    const int pr = EPI == MM_DGATE ? 0 : i;
+    if (p.y[i]) ok = ok && out_map(&maps.y[i], p.y[i], p.N[pr], 1, p.M[pr], p.ldy[pr]);
+  }
+  if (EPI == MM_LINEAR && p.res && p.vec) ok = ok && out_map(&maps.x, p.res, p.N[0], 1, p.M[0], p.ld_res);
+  if (EPI != MM_LINEAR && p.gu) ok = ok && out_map(&maps.x, p.gu, p.N[0], 2, p.M[0], 2l * p.N[0]);
+  if (!ok) return -2;
   const long tiles = mm_count_tiles(p, 256, MM_BN / W_DIV);
   const int workers = static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
   launch_pdl(kern, dim3(2 * workers), dim3(MM_THREADS), MM_SMEM, st, 2, maps, p);
@@ -1039,6 +1198,7 @@ int launch_gate_up(const GateUpParams& q, cudaStream_t st) {
   p.N[0] = q.F;
   p.num_kb[0] = (q.H + 63) / 64;
   p.y[0] = q.h;
+  p.ldy[0] = q.F;
   p.act = q.act;
   p.gu = q.gu;
   const MmOperand a{q.x, q.M, q.H, q.ldx};
@@ -1053,9 +1213,10 @@ int launch_gated_dh(const GatedBackwardParams& q, cudaStream_t st) {
   p.num_kb[0] = (q.H + 63) / 64;
   p.act = q.act;
   p.gu = const_cast<uint16_t*>(q.gu);
-  p.dg = q.dg;
-  p.du = q.du;
-  p.h = q.ddown ? q.h : nullptr;
+  p.y[0] = q.dg;
+  p.y[1] = q.du;
+  p.y[2] = q.ddown ? q.h : nullptr;
+  p.ldy[0] = q.F;
   const MmOperand a{q.dy, q.M, q.H, q.ld_dy}, b{q.down, q.H, q.F, q.F};
   return mm_launch<false, true, MM_DGATE>(&a, &b, 1, 1, p, q.num_sms, st);
 }
