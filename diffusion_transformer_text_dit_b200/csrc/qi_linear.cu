@@ -17,14 +17,16 @@
 // Warp roles in a 320-thread CTA: warp 0 TMA producer, warp 1 TMEM allocator
 // and MMA issuer, warps 2..9 epilogue (warp w reads TMEM lanes 32 (w % 4) .. +
 // 31; two warps share a lane quarter).  Large products run on persistent CTA
-// pairs with 256 x 256 tiles (mm_kernel), middle ones on 128 x 128 tiles whose
-// K a cluster shares (mm_split_kernel), up to 32 rows of A on warp-level MMAs
-// that stream the weights (skinny_kernel).  MM_GATE takes half of the B rows
-// from each weight, so a tile holds gate columns next to the same up columns
-// and their product never leaves the registers; in a pair, each CTA loads one
-// weight.
+// pairs with 256 x 256 tiles (mm_kernel), or with K shared by a cluster when
+// the tiles are few (mm_split_kernel); some hundreds of rows as the narrow
+// operand next to 128 rows of the weights (mm_rows_kernel); up to 32 rows on
+// warp-level MMAs that stream the weights (skinny_kernel).  MM_GATE takes half
+// of the weight rows of a tile from each weight, so a tile holds gate columns
+// next to the same up columns and their product never leaves the SM; in a
+// pair, each CTA loads one weight.
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "qi_common.cuh"
@@ -71,6 +73,15 @@ constexpr int MM_OUT = 32 * 64;      // bytes of an epilogue warp's stage: 32 ro
 constexpr int MM_SMEM = 1024 + MM_STAGES * 2 * MM_TILE + MM_EPI_WARPS * 2 * MM_OUT + 256;
 static_assert(2 * MM_STAGES + 6 + MM_EPI_WARPS <= 32, "barrier area");
 static_assert(MM_SMEM <= 232448, "shared memory per CTA");
+
+// Execution barrier of a cluster that orders no memory: at the end of a kernel
+// the CTAs only wait for each other's reads, and a releasing arrive would wait
+// for this CTA's output stores too (0.3 us).
+__device__ __forceinline__ void cluster_sync_end() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
+  __syncwarp();
+}
 
 // ---------------------------------------------------------------- activations
 
@@ -602,7 +613,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   // Neither CTA of a pair leaves (or frees TMEM) while the other may still read
   // its shared memory, arrive on its barriers, or have MMAs writing its TMEM.
   tc_fence_before();
-  cluster_sync_all();
+  cluster_sync_end();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 2 * MM_BN);
@@ -611,25 +622,18 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
 
 // ---------------------------------------------------------------- middle sizes
 //
-// Too few 256 x 256 tiles to fill the GPU: K is shared as well.  A cluster
-// computes one tile, its S parts each over a part of K: S pairs of CTAs on a
-// 256 x 256 tile (PAIR), or S single CTAs on a 128 x 128 tile when there are
-// at most 128 rows (two CTAs per SM then, so one's loads and MMAs lie under
-// the other's start and end).  When its MMAs are done, a CTA puts its fp32
-// sums into its shared memory; after a cluster barrier every CTA adds up a
-// share of the columns over the S parts' shared memory, in the order of K,
-// and runs the epilogue on them.  Nothing goes through memory and the result
-// does not depend on timing.
+// Too few 256 x 256 tiles to fill the GPU: K is shared as well.  A cluster of S
+// pairs of CTAs computes one tile, each pair over a part of K.  When its MMAs
+// are done, a CTA puts its fp32 sums into its shared memory; after a cluster
+// barrier every CTA adds up a share of the columns over the S parts' shared
+// memory, in the order of K, and runs the epilogue on them.  Nothing goes
+// through memory and the result does not depend on timing.
 // The sums lie as [groups of 4 columns][128 rows] of float4: the lanes of a
 // warp hold consecutive rows and touch 512 contiguous bytes.
-template <bool PAIR>
-struct MsCfg {
-  static constexpr int STAGES = PAIR ? 6 : 3;
-  static constexpr int COLS = PAIR ? 256 : 128;   // accumulator columns
-  static constexpr int SMEM = 1024 + STAGES * 2 * MM_TILE + 256;
-  static_assert(PAIR || 2 * (SMEM + 1024) <= 233472, "two CTAs per SM");
-  static_assert(128 * COLS * 4 <= STAGES * 2 * MM_TILE, "the sums over the stages");
-};
+// (Sending each share as a bulk copy into its owner's shared memory instead of
+// reading it there took 0.7 us longer.)
+constexpr int MS_SMEM = 1024 + MM_STAGES * 2 * MM_TILE + 256;
+static_assert(128 * MM_BN * 4 <= MM_STAGES * 2 * MM_TILE, "the sums over the stages");
 
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   float4 v;
@@ -639,19 +643,17 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   return v;
 }
 
-template <bool PAIR, bool AMN, bool BMN, int EPI>
-__global__ void __launch_bounds__(MM_THREADS, PAIR ? 1 : 2)
+template <bool AMN, bool BMN, int EPI>
+__global__ void __launch_bounds__(MM_THREADS, 1)
     mm_split_kernel(const __grid_constant__ MmMaps maps, const __grid_constant__ MmParams p, const int S) {
-  using C = MsCfg<PAIR>;
-  constexpr int STAGES = C::STAGES;
-  constexpr int BM = PAIR ? 256 : 128;
-  constexpr int W = EPI == MM_GATE ? C::COLS / 2 : C::COLS;   // output columns of a tile
+  constexpr int STAGES = MM_STAGES;
+  constexpr int W = EPI == MM_GATE ? MM_BN / 2 : MM_BN;   // output columns of a tile
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES * MM_TILE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * 2 * MM_TILE);   // [STAGES] (pair: even CTA's)
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * 2 * MM_TILE);   // [STAGES] (the even CTA's)
   uint64_t* empty = full + STAGES;                                             // [STAGES]
   uint64_t* tfull = empty + STAGES;
   uint64_t* drain = tfull + 1;
@@ -659,11 +661,10 @@ __global__ void __launch_bounds__(MM_THREADS, PAIR ? 1 : 2)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int ctas = PAIR ? 2 * S : S;   // of the cluster
-  const uint32_t crank = ctas > 1 ? cluster_rank() : 0u;
-  const uint32_t even = PAIR ? crank & ~1u : crank;          // the CTA that issues this one's MMAs
-  const int rank = PAIR ? static_cast<int>(crank & 1u) : 0;  // half of the tile's rows
-  const int part = static_cast<int>(PAIR ? crank >> 1 : crank);
+  const uint32_t crank = cluster_rank();
+  const uint32_t even = crank & ~1u;                // the CTA that issues this one's MMAs
+  const int rank = static_cast<int>(crank & 1u);    // half of the tile's rows
+  const int part = static_cast<int>(crank >> 1);
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -674,23 +675,17 @@ __global__ void __launch_bounds__(MM_THREADS, PAIR ? 1 : 2)
     fence_mbar_init();
   }
   if (warp == 1) {
-    if (PAIR) {
-      tmem_alloc_pair(tmem_slot, C::COLS);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(tmem_slot, C::COLS);
-      tmem_relinquish();
-    }
+    tmem_alloc_pair(tmem_slot, MM_BN);
+    tmem_relinquish_pair();
   }
   int pr, mt, nt;
-  mm_tile<BM, W>(p, static_cast<int>(blockIdx.x) / ctas, pr, mt, nt);
+  mm_tile<256, W>(p, static_cast<int>(blockIdx.x) / (2 * S), pr, mt, nt);
   const int total_kb = p.num_kb[pr] * p.segs;
   const int lo = total_kb * part / S, hi = total_kb * (part + 1) / S;
-  const int m0 = mt * BM + rank * 128;
+  const int m0 = mt * 256 + rank * 128;
   const int n0 = EPI == MM_GATE ? nt * W : nt * W + rank * 128;   // first row of B of this CTA
   tc_fence_before();
-  if (PAIR) cluster_sync_all();   // barriers of both CTAs initialised before any remote arrive
-  else __syncthreads();
+  cluster_sync_all();   // barriers of both CTAs initialised before any remote arrive
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();
@@ -705,15 +700,10 @@ __global__ void __launch_bounds__(MM_THREADS, PAIR ? 1 : 2)
       if (!mbar_wait_warp(&empty[stage], phase ^ 1u, p.status)) { ok = false; break; }
       const int seg = kb >= p.num_kb[pr] ? 1 : 0;   // segs == 2 only for a single product
       const int k = (kb - seg * p.num_kb[pr]) * 64;
-      const uint32_t fb = PAIR ? mapa_shared(smem_u32(&full[stage]), even) : smem_u32(&full[stage]);
-      if (rank == 0) mbar_expect_elect(&full[stage], (PAIR ? 4 : 2) * MM_TILE);
-      mm_load<PAIR, AMN>(&maps.a[pr + seg], fb, sA + stage * MM_TILE, k, m0);
-      if (EPI == MM_GATE && !PAIR) {
-        mm_load<PAIR, false>(&maps.b[0], fb, sB + stage * MM_TILE, k, n0);
-        mm_load<PAIR, false>(&maps.b[1], fb, sB + stage * MM_TILE + MM_TILE / 2, k, n0);
-      } else {
-        mm_load<PAIR, BMN>(&maps.b[EPI == MM_GATE ? rank : pr + seg], fb, sB + stage * MM_TILE, k, n0);
-      }
+      const uint32_t fb = mapa_shared(smem_u32(&full[stage]), even);
+      if (rank == 0) mbar_expect_elect(&full[stage], 4 * MM_TILE);
+      mm_load<true, AMN>(&maps.a[pr + seg], fb, sA + stage * MM_TILE, k, m0);
+      mm_load<true, BMN>(&maps.b[EPI == MM_GATE ? rank : pr + seg], fb, sB + stage * MM_TILE, k, n0);
       if (++stage == STAGES) { stage = 0; phase ^= 1u; }
     }
     if (!ok) {   // the loads in flight must land before the CTA exits (see mm_kernel)
@@ -731,9 +721,9 @@ __global__ void __launch_bounds__(MM_THREADS, PAIR ? 1 : 2)
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (pair: even CTA)
+    // ------------------------------------------------------------ MMA issuer (even CTA)
     if (rank == 0) {
-      constexpr uint32_t idesc = mm_idesc<PAIR, AMN, BMN>();
+      constexpr uint32_t idesc = mm_idesc<true, AMN, BMN>();
       const uint64_t adesc = mm_desc<AMN>(sA), bdesc = mm_desc<BMN>(sB);
       const uint16_t both = static_cast<uint16_t>(0x3u << even);
       int stage = 0;
@@ -742,14 +732,14 @@ __global__ void __launch_bounds__(MM_THREADS, PAIR ? 1 : 2)
         if (!mbar_wait_warp(&full[stage], phase, p.status)) { ok = false; break; }
         tc_fence_after();
         const uint64_t off = static_cast<uint64_t>(stage * (MM_TILE >> 4));
-        mm_block<PAIR, AMN, BMN>(tmem_base, adesc + off, bdesc + off, idesc, kb == lo);
-        umma_commit_elect<PAIR>(&empty[stage], both);
+        mm_block<true, AMN, BMN>(tmem_base, adesc + off, bdesc + off, idesc, kb == lo);
+        umma_commit_elect<true>(&empty[stage], both);
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
       if (ok) {
-        umma_commit_elect<PAIR>(tfull, both);
+        umma_commit_elect<true>(tfull, both);
       } else {
-        umma_commit_elect<PAIR>(drain, static_cast<uint16_t>(0x1u << even));
+        umma_commit_elect<true>(drain, static_cast<uint16_t>(0x1u << even));
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < QI_WAIT_NS) {
         }
@@ -765,7 +755,7 @@ __global__ void __launch_bounds__(MM_THREADS, PAIR ? 1 : 2)
     const bool none = lo == hi;   // no K block for this part: TMEM was not written
     if (ok)
 #pragma unroll 1
-      for (int c = half * (C::COLS / 64); c < (half + 1) * (C::COLS / 64); ++c) {
+      for (int c = half * (MM_BN / 64); c < (half + 1) * (MM_BN / 64); ++c) {
         uint32_t r[32];
         tmem_ld32(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + c * 32, r);
 #pragma unroll
@@ -777,16 +767,14 @@ __global__ void __launch_bounds__(MM_THREADS, PAIR ? 1 : 2)
       }
   }
   tc_fence_before();
-  if (ctas > 1) cluster_sync_all();
-  else __syncthreads();
+  cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    if (PAIR) tmem_dealloc_pair(tmem_base, C::COLS);
-    else tmem_dealloc(tmem_base, C::COLS);
+    tmem_dealloc_pair(tmem_base, MM_BN);
   }
   if (warp >= 2 && ok) {
     // columns [part W / S, + W / S) of this CTA's rows, 8 of a row at a time; a
-    // warp takes 8 rows x 32 columns (16 x 16), so its accesses are whole sectors
+    // warp takes 8 rows x 32 columns, so its accesses are whole sectors
     const int ng = W / S / 8;
 #pragma unroll 1
     for (int item = threadIdx.x - 64; item < 128 * ng; item += 256) {
@@ -799,8 +787,7 @@ __global__ void __launch_bounds__(MM_THREADS, PAIR ? 1 : 2)
       for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.f;
 #pragma unroll 2
       for (int s = 0; s < S; ++s) {
-        const uint32_t peer = static_cast<uint32_t>(PAIR ? 2 * s + rank : s);
-        const uint32_t from = (ctas > 1 ? mapa_shared(mine, peer) : mine) + (c >> 2) * 2048;
+        const uint32_t from = mapa_shared(mine, static_cast<uint32_t>(2 * s + rank)) + (c >> 2) * 2048;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float4 x = ld_cluster4(from + e * 2048);
@@ -820,7 +807,179 @@ __global__ void __launch_bounds__(MM_THREADS, PAIR ? 1 : 2)
       mm_out8<EPI>(p, pr, m0 + row, nt * W + c, v, u);
     }
   }
-  if (ctas > 1) cluster_sync_all();   // no CTA leaves while another may read its sums
+  cluster_sync_end();   // no CTA leaves while another may read its sums
+}
+
+// ---------------------------------------------------------------- some hundreds of rows
+//
+// The weights take the 128-row side of the MMA and T rows of a (M, or an equal
+// part of it, rounded up to 16) the other one: no tile is half empty, and of
+// the shared memory that a K block takes 16 KB are weights on their way, whose
+// reading bounds the product.  D[n, m] = sum_k w(n, k) a(m, k): a lane of TMEM is an
+// output column, a TMEM column a row of y.  K is shared by a cluster of S CTAs
+// as above; a CTA finishes the rows part, part + S, ...
+constexpr int MR_MAX_T = 256;
+constexpr int MR_MAX_TILES = 2;   // along M: three and more were never faster than 256 x 256 tiles
+constexpr int MR_MAX_STAGES = 8;
+
+__host__ __device__ constexpr int mr_stage(int T) { return MM_TILE + T * 128; }
+__host__ __device__ constexpr int mr_area(int T, int stages) {
+  return stages * mr_stage(T) > 512 * T ? stages * mr_stage(T) : 512 * T;   // the sums lie over the stages
+}
+static int mr_smem(int T, int stages) { return 1024 + mr_area(T, stages) + 256; }
+
+template <bool WMN, int EPI>
+__global__ void __launch_bounds__(MM_THREADS, 2)
+    mm_rows_kernel(const __grid_constant__ MmMaps maps, const __grid_constant__ MmParams p, const int S, const int T,
+                   const int stages) {
+  constexpr int W = EPI == MM_GATE ? 64 : 128;   // output columns of a tile
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + mr_area(T, stages));   // [MR_MAX_STAGES]
+  uint64_t* empty = full + MR_MAX_STAGES;                                    // [MR_MAX_STAGES]
+  uint64_t* tfull = empty + MR_MAX_STAGES;
+  uint64_t* drain = tfull + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = S > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const uint32_t cols = T <= 64 ? 64 : (T <= 128 ? 128 : 256);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, cols);
+    tmem_relinquish();
+  }
+  const int tile = static_cast<int>(blockIdx.x) / S, m_tiles = (p.M[0] + T - 1) / T;
+  const int n0 = tile / m_tiles * W, m0 = tile % m_tiles * T;
+  const int rows = min(T, p.M[0] - m0);
+  const int total_kb = p.num_kb[0] * p.segs;
+  const int lo = total_kb * part / S, hi = total_kb * (part + 1) / S;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  bool ok = true;
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (the whole warp, one lane issues)
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = lo; kb < hi; ++kb) {
+      if (!mbar_wait_warp(&empty[stage], phase ^ 1u, p.status)) { ok = false; break; }
+      const int seg = kb >= p.num_kb[0] ? 1 : 0;
+      const int k = (kb - seg * p.num_kb[0]) * 64;
+      const uint32_t fb = smem_u32(&full[stage]);
+      uint8_t* dst = smem + stage * mr_stage(T);
+      mbar_expect_elect(&full[stage], static_cast<uint32_t>(mr_stage(T)));
+      if (EPI == MM_GATE) {
+        mm_load<false, false>(&maps.a[0], fb, dst, k, n0);
+        mm_load<false, false>(&maps.a[1], fb, dst + MM_TILE / 2, k, n0);
+      } else {
+        mm_load<false, WMN>(&maps.a[seg], fb, dst, k, n0);
+      }
+      mm_load<false, false>(&maps.b[seg], fb, dst + MM_TILE, k, m0);
+      if (++stage == stages) { stage = 0; phase ^= 1u; }
+    }
+    if (!ok) {   // the loads in flight must land before the CTA exits
+      for (int s = 0; s < stages; ++s) {
+        const uint32_t par = (s < stage) ? phase : (phase ^ 1u);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(&full[s], par) && globaltimer_ns() - t0 < QI_WAIT_NS) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t idesc = umma_idesc(false, 128, T) | (WMN ? (1u << 15) : 0u);
+    const uint64_t adesc = mm_desc<WMN>(smem), bdesc = mm_desc<false>(smem + MM_TILE);
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = lo; kb < hi; ++kb) {
+      if (!mbar_wait_warp(&full[stage], phase, p.status)) { ok = false; break; }
+      tc_fence_after();
+      const uint64_t off = static_cast<uint64_t>(stage * (mr_stage(T) >> 4));
+      mm_block<false, WMN, false>(tmem_base, adesc + off, bdesc + off, idesc, kb == lo);
+      umma_commit_elect<false>(&empty[stage]);
+      if (++stage == stages) { stage = 0; phase ^= 1u; }
+    }
+    if (ok) {
+      umma_commit_elect<false>(tfull);
+    } else {
+      umma_commit_elect<false>(drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < QI_WAIT_NS) {
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ this CTA's sums into its shared memory: [T][128]
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    float* sums = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
+    ok = mbar_wait_warp(tfull, 0, p.status);
+    tc_fence_after();
+    const bool none = lo == hi;   // no K block for this part: TMEM was not written
+    if (ok)
+#pragma unroll 1
+      for (int c = half * 32; c < T; c += 64) {
+        uint32_t r[32];
+        tmem_ld32(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + c, r);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < 16 || c + 16 < T) sums[(c + i) * 128] = none ? 0.f : __uint_as_float(r[i]);
+      }
+  }
+  tc_fence_before();
+  if (S > 1) cluster_sync_all();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, cols);
+  }
+  if (warp >= 2 && ok) {
+    // 8 columns of a row at a time, whole rows of the tile per warp
+    constexpr int NG = W / 8;
+    const uint32_t mine = smem_u32(smem);
+#pragma unroll 1
+    for (int item = threadIdx.x - 64;; item += 256) {
+      const int m = part + S * (item / NG), g = item % NG;
+      if (m >= rows) break;
+      float v[8], u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.f;
+#pragma unroll 2
+      for (int s = 0; s < S; ++s) {
+        const uint32_t from = (S > 1 ? mapa_shared(mine, static_cast<uint32_t>(s)) : mine) +
+                              static_cast<uint32_t>(m) * 512 + g * 32;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 x = ld_cluster4(from + e * 16);
+          v[4 * e] += x.x;
+          v[4 * e + 1] += x.y;
+          v[4 * e + 2] += x.z;
+          v[4 * e + 3] += x.w;
+          if (EPI == MM_GATE) {
+            const float4 y = ld_cluster4(from + 256 + e * 16);   // the up columns, 64 further on
+            u[4 * e] += y.x;
+            u[4 * e + 1] += y.y;
+            u[4 * e + 2] += y.z;
+            u[4 * e + 3] += y.w;
+          }
+        }
+      }
+      mm_out8<EPI>(p, 0, m0 + m, n0 + g * 8, v, u);
+    }
+  }
+  if (S > 1) cluster_sync_end();   // no CTA leaves while another may read its sums
 }
 
 // ---------------------------------------------------------------- few rows
@@ -1042,62 +1201,83 @@ static int cluster_places(K kern, int ctas, int smem, int num_sms) {
   return n;
 }
 
-// Kernel of a launch.  The estimate is in clocks: rounds of tiles times K
-// blocks times the clocks of a block, plus about 15000 for what starts and ends
-// a tile (the launch, the first loads, the sums' way out; the persistent kernel
-// pays it once).  A K block of a pair's tile takes about 600 clocks (32 KB into
-// each SM); one of a 128 x 128 tile about as long, for half the work per SM.
-// Measured, whole K / parts of K: 64 x 4096 x 4096 15.2 / 12.7 us, 64 x
-// 4096 x 11008 34 / 23 us, 512 x 4096 x 11008 55 / 38 us.
+// Kernel of a launch, by estimates in clocks.
+// 256 x 256 tiles: rounds of tiles times K blocks times 600 (32 KB into each
+// SM), plus what starts and ends a tile (the launch, the first loads, the sums'
+// way out): 14000, which the persistent kernel pays once, or per round 15000
+// with shared K, 23000 with the five accesses of MM_DGATE.  Measured, whole K /
+// parts of K: 512 x 4096 x 11008 55 / 38 us.
+// mm_rows_kernel: 8000 per round and 9 S T for the exchange, plus the largest of
+//   a CTA's K blocks, each its loads' latency (340, or 2000 over the stages) or
+//   its bytes at 84 per clock;
+//   all CTAs' loads, which L2 gives at 9000 bytes per clock;
+//   the weights, which memory gives at 3400.
+// Measured, 256 x 256 tiles / this kernel: 64 x 4096 x 4096 16.8 / 11.2 us, 128
+// x 22016 x 4096 51 / 39, 333 x 4096 x 4096 19.7 / 15.8; 256 x 6144 x 4096 19.9
+// / 20.5, 512 x 6144 x 4096 27.8 / 30.
 struct MmShape {
-  bool pair;
-  int S;   // parts of K (pair with 1: the persistent kernel)
+  bool rows;    // mm_rows_kernel
+  int S;        // parts of K (1 and not rows: the persistent kernel)
+  int T, stages;
 };
 template <bool AMN, bool BMN, int EPI>
 static bool mm_shape(MmParams p, int num_sms, MmShape* pick) {
   constexpr int W_DIV = EPI == MM_GATE ? 2 : 1;
-  static std::atomic<uint64_t> done_p{0}, done_s{0};
-  auto pair_kern = mm_split_kernel<true, AMN, BMN, EPI>;
-  auto single_kern = mm_split_kernel<false, AMN, BMN, EPI>;
-  if (!allow_smem(pair_kern, MsCfg<true>::SMEM, done_p) || !allow_smem(single_kern, MsCfg<false>::SMEM, done_s))
-    return false;
-  long kb = 0, rows = 0;
-  for (int i = 0; i < p.n_prob; ++i) {
-    kb = kb > p.num_kb[i] * p.segs ? kb : p.num_kb[i] * p.segs;
-    rows = rows > p.M[i] ? rows : p.M[i];
-  }
+  static std::atomic<uint64_t> done_p{0};
+  auto pair_kern = mm_split_kernel<AMN, BMN, EPI>;
+  if (!allow_smem(pair_kern, MS_SMEM, done_p)) return false;
+  long kb = 0;
+  for (int i = 0; i < p.n_prob; ++i) kb = kb > p.num_kb[i] * p.segs ? kb : p.num_kb[i] * p.segs;
   auto rounds = [](long n, long places) { return (n + places - 1) / places; };
   const long tiles = mm_count_tiles(p, 256, 256 / W_DIV);
   long best = rounds(tiles, num_sms / 2) * kb * 600 + 14000;
-  *pick = {true, 1};
+  *pick = {false, 1, 0, 0};
   for (int s = 2; s <= 4; s *= 2) {
-    const long cost = rounds(tiles, cluster_places(pair_kern, 2 * s, MsCfg<true>::SMEM, num_sms)) *
-                          (rounds(kb, s) * 600 + 15000);
+    const long cost = rounds(tiles, cluster_places(pair_kern, 2 * s, MS_SMEM, num_sms)) *
+                          (rounds(kb, s) * 600 + (EPI == MM_DGATE ? 23000 : 15000));
     if (cost < best) {
       best = cost;
-      *pick = {true, s};
+      *pick = {false, s, 0, 0};
     }
   }
-  if (rows <= 128) {
-    const long t1 = mm_count_tiles(p, 128, 128 / W_DIV);
-    for (int s = 1; s <= (EPI == MM_GATE ? 4 : 8); s *= 2) {
-      const long cost = rounds(t1, cluster_places(single_kern, s, MsCfg<false>::SMEM, num_sms)) *
-                            (rounds(kb, s) * (500 + 100 * rows / 128) + 15000);
-      if (cost < best) {
-        best = cost;
-        *pick = {false, s};
+  if constexpr (!AMN) {
+    static std::atomic<uint64_t> done_r{0};
+    auto kern = mm_rows_kernel<BMN, EPI>;
+    if (!allow_smem(kern, 232448, done_r)) return false;
+    const int m_tiles = (p.M[0] + MR_MAX_T - 1) / MR_MAX_T;
+    if (m_tiles <= MR_MAX_TILES) {
+      const int T = ((p.M[0] + m_tiles - 1) / m_tiles + 15) / 16 * 16;
+      const long nw = rounds(p.N[0], 128 / W_DIV), n = nw * rounds(p.M[0], T);
+      for (int s = 1; s <= 8; s *= 2) {
+        // two CTAs per SM when there are more CTAs than SMs and TMEM and shared memory allow it
+        const int per_sm = T <= 128 && n * s > num_sms ? 2 : 1;
+        const int stages = std::min(MR_MAX_STAGES, ((per_sm == 2 ? 115712 : 232448) - 1280) / mr_stage(T));
+        const long r = rounds(n, static_cast<long>(per_sm) * cluster_places(kern, s, mr_smem(T, stages), num_sms));
+        const long block = std::max(mr_stage(T) / 84, std::max(340, 2000 / stages));
+        const long cost = r * (8000 + 9 * s * T) + std::max(r * rounds(kb, s) * block,
+                                                            std::max(n * kb * mr_stage(T) / 9000, nw * kb * MM_TILE / 3400));
+        if (cost < best) {
+          best = cost;
+          *pick = {true, s, T, stages};
+        }
       }
     }
   }
   return true;
 }
 
-template <bool PAIR, bool AMN, bool BMN, int EPI>
-static int mm_launch_split(const MmMaps& maps, MmParams p, int S, cudaStream_t st) {
-  auto kern = mm_split_kernel<PAIR, AMN, BMN, EPI>;
-  const long tiles = mm_count_tiles(p, PAIR ? 256 : 128, MsCfg<PAIR>::COLS / (EPI == MM_GATE ? 2 : 1));
-  const unsigned ctas = static_cast<unsigned>(PAIR ? 2 * S : S);
-  launch_pdl(kern, dim3(static_cast<unsigned>(tiles) * ctas), dim3(MM_THREADS), MsCfg<PAIR>::SMEM, st, ctas, maps, p, S);
+template <bool WMN, int EPI>
+static int mm_launch_rows(const MmOperand* A, const MmOperand* B, int n_ops_a, int n_ops_b, MmParams p, MmShape s,
+                          cudaStream_t st) {
+  MmMaps maps;   // (a: the weights)
+  for (int i = 0; i < 2; ++i) {
+    if (!mm_map(&maps.a[i], B[i < n_ops_b ? i : 0], WMN, EPI == MM_GATE ? 64 : 128)) return -2;
+    if (!mm_map(&maps.b[i], A[i < n_ops_a ? i : 0], false, s.T)) return -2;
+  }
+  const unsigned tiles = static_cast<unsigned>((p.N[0] + (EPI == MM_GATE ? 63 : 127)) / (EPI == MM_GATE ? 64 : 128) *
+                                               ((p.M[0] + s.T - 1) / s.T));
+  launch_pdl(mm_rows_kernel<WMN, EPI>, dim3(tiles * s.S), dim3(MM_THREADS), mr_smem(s.T, s.stages), st, s.S, maps, p,
+             s.S, s.T, s.stages);
   return launch_result();
 }
 
@@ -1110,13 +1290,19 @@ static int mm_launch(const MmOperand* A, const MmOperand* B, int n_ops_a, int n_
     launch_result();
     return -1;
   }
+  if constexpr (!AMN)
+    if (shape.rows) return mm_launch_rows<BMN, EPI>(A, B, n_ops_a, n_ops_b, p, shape, st);
   MmMaps maps;
   for (int i = 0; i < MM_MAX_PROB; ++i) {
     if (!mm_map(&maps.a[i], A[i < n_ops_a ? i : 0], AMN, 128)) return -2;
-    if (!mm_map(&maps.b[i], B[i < n_ops_b ? i : 0], BMN, !shape.pair && EPI == MM_GATE ? 64 : 128)) return -2;
+    if (!mm_map(&maps.b[i], B[i < n_ops_b ? i : 0], BMN, 128)) return -2;
   }
-  if (!shape.pair) return mm_launch_split<false, AMN, BMN, EPI>(maps, p, shape.S, st);
-  if (shape.S > 1) return mm_launch_split<true, AMN, BMN, EPI>(maps, p, shape.S, st);
+  const long tiles = mm_count_tiles(p, 256, MM_BN / W_DIV);
+  if (shape.S > 1) {
+    launch_pdl(mm_split_kernel<AMN, BMN, EPI>, dim3(static_cast<unsigned>(tiles) * 2 * shape.S), dim3(MM_THREADS),
+               MS_SMEM, st, static_cast<unsigned>(2 * shape.S), maps, p, shape.S);
+    return launch_result();
+  }
   auto kern = mm_kernel<AMN, BMN, EPI>;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kern, MM_SMEM, done)) {
@@ -1134,7 +1320,6 @@ static int mm_launch(const MmOperand* A, const MmOperand* B, int n_ops_a, int n_
   if (EPI == MM_LINEAR && p.res && p.vec) ok = ok && out_map(&maps.x, p.res, p.N[0], 1, p.M[0], p.ld_res);
   if (EPI != MM_LINEAR && p.gu) ok = ok && out_map(&maps.x, p.gu, p.N[0], 2, p.M[0], 2l * p.N[0]);
   if (!ok) return -2;
-  const long tiles = mm_count_tiles(p, 256, MM_BN / W_DIV);
   const int workers = static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
   launch_pdl(kern, dim3(2 * workers), dim3(MM_THREADS), MM_SMEM, st, 2, maps, p);
   return launch_result();
