@@ -291,8 +291,10 @@ struct LinearActParams {
   int ldy;
   int num_sms;
   int* status;
+  bool after_tiles;       // follows launch_gate_up, which ran on tensor-core tiles
 };
 int launch_linear_act(const LinearActParams& p, cudaStream_t st);
+bool gate_up_on_tiles(int M, int H, int F, int num_sms);
 
 // Gate and up projections with the activation and the product in one kernel:
 //   h = bf16(act(x gate^T) * (x up^T)), optionally gu = bf16(x gate^T | x up^T)

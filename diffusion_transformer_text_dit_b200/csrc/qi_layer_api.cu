@@ -206,6 +206,7 @@ int qi_linear_act(qi_ctx* ctx, const uint16_t* a, int M, int lda, const qi_linea
   p.ldy = ldy;
   p.num_sms = ctx->num_sms;
   p.status = ctx->status;
+  p.after_tiles = false;
   DeviceScope dev(ctx);
   if (!dev.ok) return cuda_fail("cudaSetDevice");
   Prof pr(ctx, QI_KCLASS_GEMM_BF16, S(stream));
@@ -324,6 +325,7 @@ int qi_gated_ffn_forward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x, 
   p.ldy = ldy;
   p.num_sms = ctx->num_sms;
   p.status = ctx->status;
+  p.after_tiles = qi::gate_up_on_tiles(M, H, F, ctx->num_sms);
   DeviceScope dev(ctx);
   if (!dev.ok) return cuda_fail("cudaSetDevice");
   {

@@ -19,7 +19,7 @@
 // 31; two warps share a lane quarter).  Large products run on persistent CTA
 // pairs with 256 x 256 tiles (mm_kernel), or with K shared by a cluster when
 // the tiles are few (mm_split_kernel); some hundreds of rows as the narrow
-// operand next to 128 rows of the weights (mm_rows_kernel); up to 32 rows on
+// operand next to 128 rows of the weights (mm_rows_kernel); a few rows on
 // warp-level MMAs that stream the weights (skinny_kernel).  MM_GATE takes half
 // of the weight rows of a tile from each weight, so a tile holds gate columns
 // next to the same up columns and their product never leaves the SM; in a
@@ -984,7 +984,7 @@ __global__ void __launch_bounds__(MM_THREADS, 2)
 
 // ---------------------------------------------------------------- few rows
 //
-// M <= 32 rows: the product is bound by reading the weights once, so the
+// A few rows (use_skinny): the product is bound by reading the weights once, so the
 // weights go straight from memory into the fragments of warp-level MMAs
 // (m16n8k16: 16 weight rows against 8 rows of a), with no staging and no
 // 128-row tile that would be almost empty.  A thread's fragment of a 32-wide
@@ -1123,16 +1123,20 @@ __global__ void __launch_bounds__(SK_THREADS, 2) skinny_kernel(const SkinnyParam
 
 // ---------------------------------------------------------------- host side
 
-// Largest dynamic shared memory of a kernel, set once per device.
+// An attribute of a kernel, set once per device.
 template <class K>
-static bool allow_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
+static bool set_once(K kern, cudaFuncAttribute attr, int value, std::atomic<uint64_t>& done) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const uint64_t bit = 1ull << (dev & 63);
   if (done.load(std::memory_order_acquire) & bit) return true;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (cudaFuncSetAttribute(kern, attr, value) != cudaSuccess) return false;
   done.fetch_or(bit, std::memory_order_release);
   return true;
+}
+template <class K>
+static bool allow_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
+  return set_once(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes, done);
 }
 
 struct MmOperand {
@@ -1325,29 +1329,53 @@ static int mm_launch(const MmOperand* A, const MmOperand* B, int n_ops_a, int n_
   return launch_result();
 }
 
-// 32 rows: against the 128-row tiles with K split over a cluster, 4096 x 4096
-// takes 9.8 us (tiles 12.7) at 20 rows and 12.2 (12.9) at 32; 4096 x 11008
-// 19.3 (23.2) and 25.2 (23.6); the gated pair of 4096 x 11008 41 (50) and 50
-// (51); 1024 x 1024 3.0 (5.6) and 3.1 (5.9).  With more rows the reads of a,
-// which every CTA makes from L2, cost more than the empty half of a tile.
-constexpr int SK_MAX_ROWS = 32;
+// Whether skinny_kernel runs a product.  It starts and ends 2 us sooner than
+// mm_rows_kernel but reads a again in every CTA and pays for rows 9 and up, so:
+// up to 8 rows; while all CTAs run at once (two per SM) up to 16, or with short
+// K 32.  Measured, this kernel / mm_rows_kernel: 1 x 4096 x 4096 8.4 / 8.8 us,
+// 1 x 6144 x 4096 9.7 / 11.2, 16 x 4096 x 4096 9.1 / 9.7, 32 x 1024 x 1024 3.0 /
+// 4.8; on the other side 16 x 6144 x 4096 14.6 / 11.6, 32 x 4096 x 4096 12 /
+// 10.4.  The gated pair, with two streams per CTA, only while all run at once:
+// feed-forward block of 1 x 1024 x 2816 9.0 / 10.2, of 1 x 4096 x 11008 50.5 /
+// 47.7, of 8 52.0 / 48.1.  The down projection of a block follows the choice for
+// its gate and up: an SM divides its memory anew between L1 and shared memory
+// from one of the kernels to the other (52.4 us with one of each).
+static bool use_skinny(int M, int N, int K, bool gate, int num_sms) {
+  const bool at_once = (N + 15) / 16 <= 2 * num_sms;
+  if (M <= 8) return at_once || !gate;
+  return at_once && (M <= 16 || (M <= 32 && K <= 1024));
+}
 
-template <bool GATE>
-static int launch_skinny(const SkinnyParams& s, cudaStream_t st) {
-  const dim3 grid((s.N + 15) / 16);
-  if (s.M <= 8) launch_pdl(skinny_kernel<1, GATE>, grid, dim3(SK_THREADS), 0, st, 1, s);
-  else if (s.M <= 16) launch_pdl(skinny_kernel<2, GATE>, grid, dim3(SK_THREADS), 0, st, 1, s);
-  else if (s.M <= 24) launch_pdl(skinny_kernel<3, GATE>, grid, dim3(SK_THREADS), 0, st, 1, s);
-  else launch_pdl(skinny_kernel<4, GATE>, grid, dim3(SK_THREADS), 0, st, 1, s);
+template <int NT, bool GATE>
+static int launch_skinny_nt(const SkinnyParams& s, cudaStream_t st) {
+  // Loads in flight need L1: without this an SM stays divided as the last kernel
+  // left it, and a product behind one that uses all of it as shared memory (1 x
+  // 4096 x 11008, 17 us) took 40 us.
+  static std::atomic<uint64_t> done{0};
+  auto kern = skinny_kernel<NT, GATE>;
+  if (!set_once(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 30, done)) {
+    launch_result();
+    return -1;
+  }
+  launch_pdl(kern, dim3((s.N + 15) / 16), dim3(SK_THREADS), 0, st, 1, s);
   return launch_result();
 }
+template <bool GATE>
+static int launch_skinny(const SkinnyParams& s, cudaStream_t st) {
+  if (s.M <= 8) return launch_skinny_nt<1, GATE>(s, st);
+  if (s.M <= 16) return launch_skinny_nt<2, GATE>(s, st);
+  if (s.M <= 24) return launch_skinny_nt<3, GATE>(s, st);
+  return launch_skinny_nt<4, GATE>(s, st);
+}
+
+bool gate_up_on_tiles(int M, int H, int F, int num_sms) { return !use_skinny(M, F, H, true, num_sms); }
 
 static bool rows16(const void* p, int ld) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0;
 }
 
 int launch_linear_act(const LinearActParams& q, cudaStream_t st) {
-  if (q.M <= SK_MAX_ROWS) {
+  if (!q.after_tiles && use_skinny(q.M, q.N, q.K, false, q.num_sms)) {
     SkinnyParams s;
     memset(&s, 0, sizeof(s));
     s.a = q.a; s.M = q.M; s.K = q.K; s.N = q.N; s.lda = q.lda;
@@ -1371,7 +1399,7 @@ int launch_linear_act(const LinearActParams& q, cudaStream_t st) {
 }
 
 int launch_gate_up(const GateUpParams& q, cudaStream_t st) {
-  if (q.M <= SK_MAX_ROWS) {
+  if (!gate_up_on_tiles(q.M, q.H, q.F, q.num_sms)) {
     SkinnyParams s;
     memset(&s, 0, sizeof(s));
     s.a = q.x; s.M = q.M; s.K = q.H; s.N = q.F; s.lda = q.ldx;

@@ -347,11 +347,11 @@ def test_linear_shapes(ctx, M, n, k):
     check_linear(ctx, a, w, b, qi.QI_ACT_GELU_TANH, rand(M, n, seed=4))
 
 
-@pytest.mark.parametrize("M", [20, 24, 25, 31, 32, 33, 95])
-@pytest.mark.parametrize("n,k", [(8, 8), (24, 72), (200, 128), (256, 192), (520, 4096), (2000, 520)])
+@pytest.mark.parametrize("M", [7, 16, 20, 24, 25, 31, 32, 33, 95, 250, 257, 400])
+@pytest.mark.parametrize("n,k", [(8, 8), (24, 72), (200, 128), (256, 192), (520, 4096), (2000, 520), (6000, 264)])
 def test_linear_few_rows(ctx, M, n, k):
-    """Around the last row count that streams the weights, and middle sizes whose K is
-    shared by several CTAs: fewer pieces of K than CTAs, unequal shares."""
+    """Around the last row counts that stream the weights, and sizes whose K is shared
+    by several CTAs: fewer pieces of K than CTAs, unequal shares, two tiles of rows."""
     a, w, b = rand(M, k), rand(n, k, seed=1, scale=0.05), rand(n, seed=2)
     check_linear(ctx, a, w, b, qi.QI_ACT_SILU, rand(M, n, seed=3))
     check_linear(ctx, a, w, None, qi.QI_ACT_NONE)
@@ -463,7 +463,7 @@ def check_backward(ctx, w, x, wg, wu, wd, act, gu, dy):
     return dict(zip(refs, got))
 
 
-SHAPES = [(1, 64, 128), (16, 200, 72), (25, 136, 328), (32, 520, 200), (33, 64, 4096), (40, 4096, 64), (17, 256, 520), (100, 512, 1384), (333, 1024, 2816), (129, 8, 8),
+SHAPES = [(1, 64, 128), (16, 200, 72), (25, 136, 328), (32, 520, 200), (33, 64, 4096), (40, 4096, 64), (9, 64, 8192), (17, 256, 520), (100, 512, 1384), (333, 1024, 2816), (129, 8, 8),
           (700, 1032, 264)]
 
 
