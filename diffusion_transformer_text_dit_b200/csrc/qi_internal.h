@@ -297,7 +297,7 @@ int launch_linear_act(const LinearActParams& p, cudaStream_t st);
 bool gate_up_on_tiles(int M, int H, int F, int num_sms);
 
 // Gate and up projections with the activation and the product in one kernel:
-//   h = bf16(act(x gate^T) * (x up^T)), optionally gu = bf16(x gate^T | x up^T)
+//   h = bf16(act(x gate^T) * (x up^T)), optionally gu = fp32 (x gate^T | x up^T)
 struct GateUpParams {
   const uint16_t* x;      // [M, ldx]
   int M, H, F, ldx;
@@ -305,7 +305,7 @@ struct GateUpParams {
   const uint16_t* up;     // [F, H]
   int act;
   uint16_t* h;            // [M, F]
-  uint16_t* gu;           // [M, 2F] or null
+  float* gu;              // [M, 2F] or null
   int num_sms;
   int* status;
 };
@@ -315,7 +315,7 @@ int launch_gate_up(const GateUpParams& p, cudaStream_t st);
 struct GatedBackwardParams {
   const uint16_t* x;      // [M, ldx]
   const uint16_t* dy;     // [M, ld_dy]
-  const uint16_t* gu;     // [M, 2F] saved gate | up
+  const float* gu;        // [M, 2F] saved gate | up
   int M, H, F, ldx, ld_dy;
   const uint16_t* gate;
   const uint16_t* up;

@@ -270,7 +270,7 @@ int qi_gated_ffn_workspace_bytes(const qi_gated_ffn* w, int M, int backward, siz
 
 int qi_gated_ffn_forward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x, int M, int ldx,
                          const uint16_t* residual, int ld_residual, uint16_t* y, int ldy,
-                         uint16_t* gate_up, void* workspace, size_t workspace_bytes, void* stream) {
+                         float* gate_up, void* workspace, size_t workspace_bytes, void* stream) {
   if (!ctx) return fail(QI_ERR_INVALID_ARG, "ctx is NULL");
   int r;
   if ((r = check_gated(w))) return r;
@@ -286,7 +286,7 @@ int qi_gated_ffn_forward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x, 
   if ((r = take_workspace(workspace, workspace_bytes, need, &c))) return r;
   const GatedBufs b = carve_gated(c, M, F, false);
   // y may be x (the input is read before y is written) or the residual itself
-  const size_t yb = span_bytes(M, H, ldy), gb = gate_up ? static_cast<size_t>(M) * 2 * F * 2 : 0,
+  const size_t yb = span_bytes(M, H, ldy), gb = gate_up ? static_cast<size_t>(M) * 2 * F * 4 : 0,
                wb = static_cast<size_t>(H) * F * 2;
   if (overlap(y, yb, workspace, workspace_bytes) || overlap(gate_up, gb, workspace, workspace_bytes) ||
       overlap(y, yb, gate_up, gb) || overlap(gate_up, gb, x, span_bytes(M, H, ldx)) ||
@@ -294,6 +294,9 @@ int qi_gated_ffn_forward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x, 
       overlap(x, span_bytes(M, H, ldx), workspace, workspace_bytes) ||
       overlap(residual, span_bytes(M, H, ld_residual), workspace, workspace_bytes) ||
       overlap(y, yb, w->down, wb) || overlap(y, yb, w->gate, wb) || overlap(y, yb, w->up, wb) ||
+      overlap(gate_up, gb, w->down, wb) || overlap(gate_up, gb, w->gate, wb) || overlap(gate_up, gb, w->up, wb) ||
+      overlap(workspace, workspace_bytes, w->down, wb) || overlap(workspace, workspace_bytes, w->gate, wb) ||
+      overlap(workspace, workspace_bytes, w->up, wb) ||
       (residual && (residual != y || ld_residual != ldy) &&
        overlap(y, yb, residual, span_bytes(M, H, ld_residual))))
     return fail(QI_ERR_INVALID_ARG, "gated ffn: an output overlaps an input, the workspace or the other output");
@@ -337,7 +340,7 @@ int qi_gated_ffn_forward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x, 
 }
 
 int qi_gated_ffn_backward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x, int M, int ldx,
-                          const uint16_t* dy, int ld_dy, const uint16_t* gate_up, uint16_t* dx,
+                          const uint16_t* dy, int ld_dy, const float* gate_up, uint16_t* dx,
                           int ld_dx, uint16_t* dgate, uint16_t* dup, uint16_t* ddown,
                           void* workspace, size_t workspace_bytes, void* stream) {
   if (!ctx) return fail(QI_ERR_INVALID_ARG, "ctx is NULL");
@@ -351,7 +354,7 @@ int qi_gated_ffn_backward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x,
       (r = check_rows("dup", dup, H, H, false)) || (r = check_rows("ddown", ddown, F, F, false)))
     return r;
   const size_t wb = static_cast<size_t>(H) * F * 2, xb = span_bytes(M, H, ldx), yb = span_bytes(M, H, ld_dy),
-               gb = static_cast<size_t>(M) * 2 * F * 2;
+               gb = static_cast<size_t>(M) * 2 * F * 4;
   struct Range {
     const void* p;
     size_t n;

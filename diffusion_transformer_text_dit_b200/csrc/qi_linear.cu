@@ -44,7 +44,7 @@ constexpr int MM_MAX_PROB = 3;
 struct MmMaps {
   CUtensorMap a[MM_MAX_PROB], b[MM_MAX_PROB];
   // persistent kernel, boxes of 32 rows x 32 columns: the outputs (MM_DGATE: dg,
-  // du, h) and the residual or gate | up
+  // du, h) and the residual (bf16) or gate | up (fp32)
   CUtensorMap y[MM_MAX_PROB], x;
 };
 
@@ -62,17 +62,24 @@ struct MmParams {
   const uint16_t* res;
   int ld_res;
   int act;
-  uint16_t* gu;                // MM_GATE: optional output, MM_DGATE: input, [M, 2F]
+  float* gu;                   // MM_GATE: optional output, MM_DGATE: input, [M, 2F]
   int* status;
 };
 
 constexpr int MM_TILE = 128 * 128;   // bytes of a stage's A or B tile of one CTA: 128 x 64 bf16
 constexpr int MM_BN = 256;           // persistent kernel: columns of a pair's tile
 constexpr int MM_STAGES = 6;
-constexpr int MM_OUT = 32 * 64;      // bytes of an epilogue warp's stage: 32 rows x 32 bf16 columns
-constexpr int MM_SMEM = 1024 + MM_STAGES * 2 * MM_TILE + MM_EPI_WARPS * 2 * MM_OUT + 256;
-static_assert(2 * MM_STAGES + 6 + MM_EPI_WARPS <= 32, "barrier area");
-static_assert(MM_SMEM <= 232448, "shared memory per CTA");
+constexpr int MM_OUT = 32 * 64;      // bytes of an epilogue chunk of 32 rows x 32 bf16 columns
+// Persistent kernel: stages of the operands, and chunks of shared memory per
+// epilogue warp (an fp32 chunk takes two; MM_DGATE holds gate and up at once).
+template <int EPI>
+struct MmCfg {
+  static constexpr int STAGES = EPI == MM_DGATE ? 5 : MM_STAGES;
+  static constexpr int CHUNKS = EPI == MM_DGATE ? 4 : 2;
+  static constexpr int SMEM = 1024 + STAGES * 2 * MM_TILE + MM_EPI_WARPS * CHUNKS * MM_OUT + 256;
+  static_assert(2 * STAGES + 6 + MM_EPI_WARPS <= 32, "barrier area");
+  static_assert(SMEM <= 232448, "shared memory per CTA");
+};
 
 // Execution barrier of a cluster that orders no memory: at the end of a kernel
 // the CTAs only wait for each other's reads, and a releasing arrive would wait
@@ -145,6 +152,23 @@ __device__ __forceinline__ void load8(const uint16_t* src, uint32_t (&pk)[4], in
   }
 }
 
+// 8 fp32 values, 16-byte aligned.
+__device__ __forceinline__ void load8f(const float* src, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 x = reinterpret_cast<const float4*>(src)[i];
+    v[4 * i] = x.x;
+    v[4 * i + 1] = x.y;
+    v[4 * i + 2] = x.z;
+    v[4 * i + 3] = x.w;
+  }
+}
+__device__ __forceinline__ void store8f(float* dst, const float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    reinterpret_cast<float4*>(dst)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
@@ -157,13 +181,14 @@ __device__ __forceinline__ void mm_tempty_signal(uint32_t addr) {
 
 // 8 output columns from their fp32 sums v (MM_GATE: and the up projection's u)
 // and inputs: the fused operation, rounded once per output.
-//   MM_LINEAR  x0 residual (with p.res); o0 = act(v + bias) + x0
-//   MM_GATE    o0 = act(v) u, o1 = v, o2 = u
-//   MM_DGATE   x0 gate, x1 up; o0 = dgate, o1 = dup, o2 = act(gate) up
+//   MM_LINEAR  x residual (with p.res); o0 = act(v + bias) + x
+//   MM_GATE    o0 = act(v) u  (v and u themselves are saved in fp32: rounded
+//              to bf16 they would double the error of the gradients)
+//   MM_DGATE   xg gate, xu up; o0 = dgate, o1 = dup, o2 = act(gate) up
 template <int EPI>
 __device__ __forceinline__ void mm_math8(const MmParams& p, float (&v)[8], const float (&u)[8], int nb, int ncols,
-                                         const uint32_t (&x0)[4], const uint32_t (&x1)[4], uint32_t (&o0)[4],
-                                         uint32_t (&o1)[4], uint32_t (&o2)[4]) {
+                                         const uint32_t (&x)[4], const float (&xg)[8], const float (&xu)[8],
+                                         uint32_t (&o0)[4], uint32_t (&o1)[4], uint32_t (&o2)[4]) {
   if constexpr (EPI == MM_LINEAR) {
     if (p.bias) {
       uint32_t b[4];
@@ -184,26 +209,23 @@ __device__ __forceinline__ void mm_math8(const MmParams& p, float (&v)[8], const
     if (p.res) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[2 * i] += bf16_lo(x0[i]);
-        v[2 * i + 1] += bf16_hi(x0[i]);
+        v[2 * i] += bf16_lo(x[i]);
+        v[2 * i + 1] += bf16_hi(x[i]);
       }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) o0[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
   } else if constexpr (EPI == MM_GATE) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i)
       o0[i] = pack_bf16x2(act_f(v[2 * i], p.act) * u[2 * i], act_f(v[2 * i + 1], p.act) * u[2 * i + 1]);
-      o1[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-      o2[i] = pack_bf16x2(u[2 * i], u[2 * i + 1]);
-    }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float u0 = bf16_lo(x1[i]), u1 = bf16_hi(x1[i]);
+      const float u0 = xu[2 * i], u1 = xu[2 * i + 1];
       float a0, a1, e0, e1;
-      act_grad_f(bf16_lo(x0[i]), p.act, a0, e0);
-      act_grad_f(bf16_hi(x0[i]), p.act, a1, e1);
+      act_grad_f(xg[2 * i], p.act, a0, e0);
+      act_grad_f(xg[2 * i + 1], p.act, a1, e1);
       o0[i] = pack_bf16x2(v[2 * i] * u0 * e0, v[2 * i + 1] * u1 * e1);
       o1[i] = pack_bf16x2(v[2 * i] * a0, v[2 * i + 1] * a1);
       o2[i] = pack_bf16x2(a0 * u0, a1 * u1);
@@ -219,44 +241,50 @@ __device__ __forceinline__ void mm_out8(const MmParams& p, int pr, int m, int nb
   const int N = p.N[pr], ncols = N - nb;
   if (ncols <= 0) return;
   const bool vec = p.vec != 0;
-  uint32_t x0[4] = {}, x1[4] = {}, o0[4], o1[4], o2[4];
-  uint16_t* row = EPI == MM_LINEAR ? nullptr : p.gu + static_cast<size_t>(m) * 2 * N + nb;
-  if (EPI == MM_LINEAR && p.res) load8(p.res + static_cast<size_t>(m) * p.ld_res + nb, x0, ncols, vec);
+  uint32_t x[4] = {}, o0[4], o1[4], o2[4];
+  float xg[8] = {}, xu[8] = {};
+  float* row = EPI == MM_LINEAR ? nullptr : p.gu + static_cast<size_t>(m) * 2 * N + nb;
+  if (EPI == MM_LINEAR && p.res) load8(p.res + static_cast<size_t>(m) * p.ld_res + nb, x, ncols, vec);
   if (EPI == MM_DGATE) {
-    load8(row, x0, ncols, true);
-    load8(row + N, x1, ncols, true);
+    load8f(row, xg);
+    load8f(row + N, xu);
   }
-  mm_math8<EPI>(p, v, u, nb, ncols, x0, x1, o0, o1, o2);
-  store8(p.y[pr] + static_cast<size_t>(m) * p.ldy[pr] + nb, o0, ncols, vec);
   if (EPI == MM_GATE && p.gu) {
-    store8(row, o1, ncols, true);
-    store8(row + N, o2, ncols, true);
+    store8f(row, v);
+    store8f(row + N, u);
   }
+  mm_math8<EPI>(p, v, u, nb, ncols, x, xg, xu, o0, o1, o2);
+  store8(p.y[pr] + static_cast<size_t>(m) * p.ldy[pr] + nb, o0, ncols, vec);
   if (EPI == MM_DGATE) {
     store8(p.y[1] + static_cast<size_t>(m) * N + nb, o1, ncols, true);
     if (p.y[2]) store8(p.y[2] + static_cast<size_t>(m) * N + nb, o2, ncols, true);
   }
 }
 
-// An epilogue warp's two stages and the barrier of its loads.
+// An epilogue warp's chunks of shared memory and the barrier of its loads.
 struct MmStage {
   uint8_t* buf;
   uint64_t* bar;
   uint32_t phase;
-  int turn;        // MM_LINEAR: chunks done, its parity is the stage
-  __device__ uint8_t* at(int i) const { return buf + (i & 1) * MM_OUT; }
+  int turn;        // chunks done; its parity is the one in use where they take turns
+  __device__ uint8_t* at(int i) const { return buf + i * MM_OUT; }
 };
 
-// Inputs of the 32 x 32 chunk at (row, col) into the stages, once the stores
-// that read them are done.
+// Inputs of the 32 x 32 chunk at (row, col) into shared memory, once the stores
+// that read it are done.  Gate and up are fp32, which the map counts as pairs
+// of 16-bit values.
 template <int EPI>
 __device__ __forceinline__ void mm_fetch(const MmMaps& maps, MmStage& s, int row, int col, int lane) {
   if (lane == 0) bulk_wait_group_read<EPI == MM_DGATE ? 0 : 1>();
   __syncwarp();
   const uint32_t bar = smem_u32(s.bar);
-  mbar_expect_elect(s.bar, EPI == MM_DGATE ? 2 * MM_OUT : MM_OUT);
-  tma_load_3d_elect(&maps.x, bar, s.at(EPI == MM_DGATE ? 0 : s.turn), col, 0, row);
-  if (EPI == MM_DGATE) tma_load_3d_elect(&maps.x, bar, s.at(1), col, 1, row);
+  mbar_expect_elect(s.bar, EPI == MM_DGATE ? 4 * MM_OUT : MM_OUT);
+  if (EPI == MM_DGATE) {
+    tma_load_3d_elect(&maps.x, bar, s.at(0), 2 * col, 0, row);
+    tma_load_3d_elect(&maps.x, bar, s.at(2), 2 * col, 1, row);
+  } else {
+    tma_load_3d_elect(&maps.x, bar, s.at(s.turn & 1), col, 0, row);
+  }
 }
 
 // One accumulator tile of the persistent kernel: rows m0 .. m0 + 127 of this
@@ -266,7 +294,8 @@ __device__ __forceinline__ void mm_fetch(const MmMaps& maps, MmStage& s, int row
 // warp's 32 x 32 chunk goes through shared memory and TMA brings the inputs and
 // takes the outputs (TMA keeps to the rows and columns that exist).  Rows that
 // are not 16-byte aligned (p.vec == 0) are accessed directly.
-// The 64-byte swizzle of a stage: 16-byte group q of row r at q ^ (r / 2 mod 4).
+// Swizzles: 16-byte group q of row r of a bf16 chunk lies at q ^ (r / 2 mod 4),
+// of an fp32 chunk at q ^ (r mod 8).
 template <int EPI>
 __device__ __forceinline__ bool mm_epilogue(const MmMaps& maps, const MmParams& p, int pr, uint64_t* tfull,
                                             uint32_t tfull_phase, uint32_t tacc, int m0, int n0, int quarter,
@@ -323,83 +352,94 @@ __device__ __forceinline__ bool mm_epilogue(const MmMaps& maps, const MmParams& 
     if (has_in) {
       if (!mbar_wait_warp(s.bar, s.phase, p.status)) return false;
       s.phase ^= 1u;
-    } else {
-      if (lane == 0) bulk_wait_group_read<1>();   // the stage's last store has read it
+    } else {   // earlier stores have read what is written next
+      if (lane == 0) {
+        if (EPI == MM_GATE && p.gu) bulk_wait_group_read<0>();
+        else bulk_wait_group_read<1>();
+      }
       __syncwarp();
     }
-    auto group = [&](uint8_t* stage, int q) {
-      return reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
+    auto group = [&](uint8_t* chunk, int q) {
+      return reinterpret_cast<uint4*>(chunk + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
     };
-    auto put = [&](uint8_t* stage, int q, const uint32_t (&o)[4]) {
-      *group(stage, q) = make_uint4(o[0], o[1], o[2], o[3]);
+    auto put = [&](uint8_t* chunk, int q, const uint32_t (&o)[4]) {
+      *group(chunk, q) = make_uint4(o[0], o[1], o[2], o[3]);
     };
-    auto send = [&](const CUtensorMap* map, const uint8_t* stage, int which) {
+    auto group_f = [&](uint8_t* chunk, int q) {
+      return reinterpret_cast<uint4*>(chunk + lane * 128 + ((q ^ (lane & 7)) << 4));
+    };
+    auto send = [&](const CUtensorMap* map, const uint8_t* chunk, int col, int which) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        tma_store_3d(map, stage, col0, which, row0);
+        tma_store_3d(map, chunk, col, which, row0);
         bulk_commit_group();
       }
     };
-    auto reuse = [&] {   // the stage of the store before the last one
-      if (lane == 0) bulk_wait_group_read<1>();
-      __syncwarp();
-    };
-    uint8_t* s0 = s.at(EPI == MM_DGATE ? 0 : s.turn);
-    uint8_t* s1 = s.at(EPI == MM_DGATE ? 1 : s.turn + 1);
-    uint32_t o0[4], o1[4], o2[EPI == MM_DGATE ? 4 : 1][4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t x0[4] = {}, x1[4] = {};
-      if (has_in) {
-        const uint4 x = *group(s0, q);
-        x0[0] = x.x; x0[1] = x.y; x0[2] = x.z; x0[3] = x.w;
-      }
-      if (EPI == MM_DGATE) {
-        const uint4 x = *group(s1, q);
-        x1[0] = x.x; x1[1] = x.y; x1[2] = x.z; x1[3] = x.w;
-      }
-      sums(q);
-      mm_math8<EPI>(p, v, u, col0 + q * 8, N - col0 - q * 8, x0, x1, o0, o1, o2[EPI == MM_DGATE ? q : 0]);
-      put(s0, q, o0);
-      if (EPI == MM_DGATE) put(s1, q, o1);
-    }
+    uint32_t x[4] = {}, o0[4], o1[4], o2[4];
+    float xg[8] = {}, xu[8] = {};
     if constexpr (EPI == MM_LINEAR) {
-      send(&maps.y[pr], s0, 0);
+      uint8_t* at = s.at(s.turn & 1);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (has_in) {
+          const uint4 w = *group(at, q);
+          x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+        }
+        sums(q);
+        mm_math8<EPI>(p, v, u, col0 + q * 8, N - col0 - q * 8, x, xg, xu, o0, o1, o2);
+        put(at, q, o0);
+      }
+      send(&maps.y[pr], at, col0, 0);
       ++s.turn;
     } else if constexpr (EPI == MM_GATE) {
-      send(&maps.y[0], s0, 0);
+      uint8_t* at = s.at(p.gu ? 0 : s.turn & 1);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        sums(q);
+        mm_math8<EPI>(p, v, u, col0 + q * 8, N - col0 - q * 8, x, xg, xu, o0, o1, o2);
+        put(at, q, o0);
+      }
+      send(&maps.y[0], at, col0, 0);
       ++s.turn;
       if (p.gu) {
-        reuse();
+        auto save = [&](const uint32_t (&t)[32], int which) {
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            o1[i] = pack_bf16x2(__uint_as_float(r[8 * q + 2 * i]), __uint_as_float(r[8 * q + 2 * i + 1]));
-          put(s1, q, o1);
-        }
-        send(&maps.x, s1, 0);
-        reuse();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            o1[i] = pack_bf16x2(__uint_as_float(r2[8 * q + 2 * i]), __uint_as_float(r2[8 * q + 2 * i + 1]));
-          put(s0, q, o1);
-        }
-        send(&maps.x, s0, 1);
-        s.turn += 2;
+          for (int q = 0; q < 8; ++q) *group_f(s.at(0), q) = make_uint4(t[4 * q], t[4 * q + 1], t[4 * q + 2], t[4 * q + 3]);
+          send(&maps.x, s.at(0), 2 * col0, which);
+        };
+        save(r, 0);
+        save(r2, 1);
       }
     } else {
-      send(&maps.y[0], s0, 0);
-      send(&maps.y[1], s1, 0);
-      if (p.y[2]) {
-        reuse();
+      uint4 g[8], h[8];   // (all read before any is overwritten: rows of the outputs are shorter)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) put(s0, q, o2[q]);
-        send(&maps.y[2], s0, 0);
+      for (int q = 0; q < 8; ++q) {
+        g[q] = *group_f(s.at(0), q);
+        h[q] = *group_f(s.at(2), q);
       }
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint4 a = g[2 * q + e], b = h[2 * q + e];
+          xg[4 * e] = __uint_as_float(a.x); xg[4 * e + 1] = __uint_as_float(a.y);
+          xg[4 * e + 2] = __uint_as_float(a.z); xg[4 * e + 3] = __uint_as_float(a.w);
+          xu[4 * e] = __uint_as_float(b.x); xu[4 * e + 1] = __uint_as_float(b.y);
+          xu[4 * e + 2] = __uint_as_float(b.z); xu[4 * e + 3] = __uint_as_float(b.w);
+        }
+        sums(q);
+        mm_math8<EPI>(p, v, u, col0 + q * 8, N - col0 - q * 8, x, xg, xu, o0, o1, o2);
+        put(s.at(0), q, o0);
+        put(s.at(1), q, o1);
+        put(s.at(2), q, o2);
+      }
+      send(&maps.y[0], s.at(0), col0, 0);
+      send(&maps.y[1], s.at(1), col0, 0);
+      if (p.y[2]) send(&maps.y[2], s.at(2), col0, 0);
     }
     if (has_in && c + 2 < CH && col0 + 64 < N) mm_fetch<EPI>(maps, s, row0, col0 + 64, lane);
   }
@@ -457,7 +497,7 @@ constexpr uint32_t mm_idesc() {
 template <bool AMN, bool BMN, int EPI>
 __global__ void __launch_bounds__(MM_THREADS, 1)
     mm_kernel(const __grid_constant__ MmMaps maps, const __grid_constant__ MmParams p) {
-  constexpr int STAGES = MM_STAGES;
+  constexpr int STAGES = MmCfg<EPI>::STAGES;
   constexpr int W = EPI == MM_GATE ? MM_BN / 2 : MM_BN;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -465,7 +505,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES * MM_TILE;
   uint8_t* sOut = smem + STAGES * 2 * MM_TILE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + MM_EPI_WARPS * 2 * MM_OUT);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + MM_EPI_WARPS * MmCfg<EPI>::CHUNKS * MM_OUT);
   uint64_t* full = bars;                     // [STAGES] (the even CTA's)
   uint64_t* empty = bars + STAGES;           // [STAGES]
   uint64_t* tfull = bars + 2 * STAGES;       // [2]
@@ -596,7 +636,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     const int half = (warp - 2) >> 2;
     int acc = 0;
     uint32_t acc_phase = 0;
-    MmStage stage{sOut + (warp - 2) * 2 * MM_OUT, &xfull[warp - 2], 0, 0};
+    MmStage stage{sOut + (warp - 2) * MmCfg<EPI>::CHUNKS * MM_OUT, &xfull[warp - 2], 0, 0};
     for (int tile = worker; tile < num_tiles; tile += workers) {
       int pr, mt, nt;
       mm_tile<256, W>(p, tile, pr, mt, nt);
@@ -607,7 +647,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
-    if (lane == 0) bulk_wait_group_read<0>();   // the stages are read before the CTA leaves
+    if (lane == 0) bulk_wait_group_read<0>();   // the chunks are read before the CTA leaves
   }
 
   // Neither CTA of a pair leaves (or frees TMEM) while the other may still read
@@ -1006,7 +1046,7 @@ struct SkinnyParams {
   int ld_res;
   uint16_t* y;
   int ldy;
-  uint16_t* gu;           // GATE: optional [M, 2N]
+  float* gu;              // GATE: optional [M, 2N]
 };
 
 // 16 bytes of a weight row: read once, not kept in L1.
@@ -1107,9 +1147,9 @@ __global__ void __launch_bounds__(SK_THREADS, 2) skinny_kernel(const SkinnyParam
     }
     if (GATE) {
       if (p.gu) {
-        uint16_t* row = p.gu + static_cast<size_t>(m) * 2 * p.N + n;
-        row[0] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
-        row[p.N] = static_cast<uint16_t>(pack_bf16x2(v2, 0.f));
+        float* row = p.gu + static_cast<size_t>(m) * 2 * p.N + n;
+        row[0] = v;
+        row[p.N] = v2;
       }
       v = act_f(v, p.act) * v2;
     } else {
@@ -1309,23 +1349,24 @@ static int mm_launch(const MmOperand* A, const MmOperand* B, int n_ops_a, int n_
   }
   auto kern = mm_kernel<AMN, BMN, EPI>;
   static std::atomic<uint64_t> done{0};
-  if (!allow_smem(kern, MM_SMEM, done)) {
+  if (!allow_smem(kern, MmCfg<EPI>::SMEM, done)) {
     launch_result();
     return -1;
   }
-  auto out_map = [](CUtensorMap* m, const void* base, int cols, int mid, int rows, long ld) {
-    return make_tmap_rows3(m, base, cols, mid, rows, static_cast<uint64_t>(ld) * 2, 32, 1, 32);
+  auto out_map = [](CUtensorMap* m, const void* base, int cols, int rows, int ld) {
+    return make_tmap_rows3(m, base, cols, 1, rows, static_cast<uint64_t>(ld) * 2, 32, 1, 32);
   };
   bool ok = true;
   for (int i = 0; i < (EPI == MM_DGATE ? 3 : p.n_prob) && p.vec; ++i) {
     const int pr = EPI == MM_DGATE ? 0 : i;
-    if (p.y[i]) ok = ok && out_map(&maps.y[i], p.y[i], p.N[pr], 1, p.M[pr], p.ldy[pr]);
+    if (p.y[i]) ok = ok && out_map(&maps.y[i], p.y[i], p.N[pr], p.M[pr], p.ldy[pr]);
   }
-  if (EPI == MM_LINEAR && p.res && p.vec) ok = ok && out_map(&maps.x, p.res, p.N[0], 1, p.M[0], p.ld_res);
-  if (EPI != MM_LINEAR && p.gu) ok = ok && out_map(&maps.x, p.gu, p.N[0], 2, p.M[0], 2l * p.N[0]);
+  if (EPI == MM_LINEAR && p.res && p.vec) ok = ok && out_map(&maps.x, p.res, p.N[0], p.M[0], p.ld_res);
+  if (EPI != MM_LINEAR && p.gu)
+    ok = ok && make_tmap_rows3(&maps.x, p.gu, 2ull * p.N[0], 2, p.M[0], 8ull * p.N[0], 64, 1, 32);
   if (!ok) return -2;
   const int workers = static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
-  launch_pdl(kern, dim3(2 * workers), dim3(MM_THREADS), MM_SMEM, st, 2, maps, p);
+  launch_pdl(kern, dim3(2 * workers), dim3(MM_THREADS), MmCfg<EPI>::SMEM, st, 2, maps, p);
   return launch_result();
 }
 
@@ -1425,7 +1466,7 @@ int launch_gated_dh(const GatedBackwardParams& q, cudaStream_t st) {
   p.N[0] = q.F;
   p.num_kb[0] = (q.H + 63) / 64;
   p.act = q.act;
-  p.gu = const_cast<uint16_t*>(q.gu);
+  p.gu = const_cast<float*>(q.gu);
   p.y[0] = q.dg;
   p.y[1] = q.du;
   p.y[2] = q.ddown ? q.h : nullptr;

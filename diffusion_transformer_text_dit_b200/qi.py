@@ -524,6 +524,22 @@ def _rows(ctx: Context, t: Optional[torch.Tensor], name: str, cols: int):
     return t.data_ptr(), ld
 
 
+def _whole(t: Optional[torch.Tensor], name: str, shape, like: torch.Tensor, dtype=torch.bfloat16):
+    """Checks a contiguous tensor of a given shape on the device of `like`."""
+    if t is not None and (tuple(t.shape) != shape or t.dtype != dtype or t.device != like.device
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {like.device}")
+
+
+def _scratch(t: Optional[torch.Tensor], like: torch.Tensor):
+    """(pointer, bytes) of a workspace tensor."""
+    if t is None:
+        return None, 0
+    if t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on {like.device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _new(shape, like: torch.Tensor, stream, dtype=torch.bfloat16):
     """An output or workspace tensor, allocated on the stream that will write it."""
     if stream is None:
@@ -577,7 +593,7 @@ def qi_attn_causal_packed(ctx: Context, q, k, v, spans: torch.Tensor, heads: int
     check(lib().qi_attn_causal_packed(
         ctx.handle, qp, ldq, q.shape[0], kp, ldk, vp, ldv, k.shape[0], heads, kv_heads, 128,
         _spans(spans), spans.shape[0], sm_scale if sm_scale is not None else 128 ** -0.5, op, ldo,
-        ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0, st))
+        *_scratch(workspace, q), st))
     return o
 
 
@@ -623,7 +639,7 @@ def qi_gated_ffn_forward(ctx: Context, w: qi_gated_ffn, x: torch.Tensor,
                          save: bool = False, gate_up: Optional[torch.Tensor] = None,
                          workspace: Optional[torch.Tensor] = None, stream=None):
     """y = (act(x gate^T) * (x up^T)) down^T + residual.  save=True (or a gate_up
-    buffer [M, 2 mlp]) also returns what the backward call needs: (y, gate_up)."""
+    buffer [M, 2 mlp] fp32) also returns what the backward call needs: (y, gate_up)."""
     st = _on(ctx, stream)
     M = x.shape[0]
     if y is None:
@@ -631,17 +647,15 @@ def qi_gated_ffn_forward(ctx: Context, w: qi_gated_ffn, x: torch.Tensor,
     if y.shape[0] != M or (residual is not None and residual.shape[0] != M):
         raise ValueError("x, residual and y must have the same number of rows")
     if save and gate_up is None:
-        gate_up = _new((M, 2 * w.mlp), x, stream)
-    if gate_up is not None and (tuple(gate_up.shape) != (M, 2 * w.mlp) or not gate_up.is_contiguous()
-                                or gate_up.dtype != torch.bfloat16):
-        raise ValueError("gate_up must be a contiguous bf16 tensor [M, 2 mlp]")
+        gate_up = _new((M, 2 * w.mlp), x, stream, torch.float32)
+    _whole(gate_up, "gate_up", (M, 2 * w.mlp), x, torch.float32)
     if workspace is None:
         workspace = _new(qi_gated_ffn_workspace_bytes(w, M), x, stream, torch.uint8)
     xp, ldx = _rows(ctx, x, "x", w.hidden)
     rp, ldr = _rows(ctx, residual, "residual", w.hidden)
     yp, ldy = _rows(ctx, y, "y", w.hidden)
     check(lib().qi_gated_ffn_forward(ctx.handle, C.byref(w), xp, M, ldx, rp, ldr, yp, ldy,
-                                     ptr(gate_up), ptr(workspace), workspace.numel(), st))
+                                     ptr(gate_up), *_scratch(workspace, x), st))
     return (y, gate_up) if gate_up is not None else y
 
 
@@ -654,8 +668,9 @@ def qi_gated_ffn_backward(ctx: Context, w: qi_gated_ffn, x: torch.Tensor, dy: to
     in `want` are not computed and come back as None."""
     st = _on(ctx, stream)
     M, H, F = x.shape[0], w.hidden, w.mlp
-    if dy.shape[0] != M or tuple(gate_up.shape) != (M, 2 * F) or gate_up.dtype != torch.bfloat16:
-        raise ValueError("dy must have x's rows and gate_up be [M, 2 mlp] bf16")
+    if dy.shape[0] != M:
+        raise ValueError("x and dy must have the same number of rows")
+    _whole(gate_up, "gate_up", (M, 2 * F), x, torch.float32)
     out = {}
     for name, t, shape in (("dx", dx, (M, H)), ("dgate", dgate, (F, H)), ("dup", dup, (F, H)),
                            ("ddown", ddown, (H, F))):
@@ -664,8 +679,10 @@ def qi_gated_ffn_backward(ctx: Context, w: qi_gated_ffn, x: torch.Tensor, dy: to
             continue
         if t is None:
             t = _new(shape, x, stream)
-        if tuple(t.shape) != shape or t.dtype != torch.bfloat16:
-            raise ValueError(f"{name} must be bf16 {shape}")
+        if name != "dx":
+            _whole(t, name, shape, x)
+        elif t.shape[0] != M:
+            raise ValueError("x and dx must have the same number of rows")
         out[name] = t
     if workspace is None:
         workspace = _new(qi_gated_ffn_workspace_bytes(w, M, True), x, stream, torch.uint8)
@@ -674,7 +691,7 @@ def qi_gated_ffn_backward(ctx: Context, w: qi_gated_ffn, x: torch.Tensor, dy: to
     op, ldo = _rows(ctx, out["dx"], "dx", H)
     check(lib().qi_gated_ffn_backward(ctx.handle, C.byref(w), xp, M, ldx, dp, ldd, ptr(gate_up), op,
                                       ldo, ptr(out["dgate"]), ptr(out["dup"]), ptr(out["ddown"]),
-                                      ptr(workspace), workspace.numel(), st))
+                                      *_scratch(workspace, x), st))
     return out["dx"], out["dgate"], out["dup"], out["ddown"]
 
 

@@ -435,24 +435,24 @@ int qi_gated_ffn_workspace_bytes(const qi_gated_ffn* w, int M, int backward, siz
 /* h = bf16(act(x Wg^T) * (x Wu^T)) (both projections, activation and product in
  * one kernel, fp32 inside), y [M, hidden] = bf16(h Wd^T + residual).
  * residual: NULL, or rows added before the rounding; residual == y (same ld)
- * and y == x are allowed.  gate_up: NULL, or [M, 2 mlp] bf16 that receives
+ * and y == x are allowed.  gate_up: NULL, or [M, 2 mlp] fp32 that receives
  * x Wg^T | x Wu^T for the backward call. */
 int qi_gated_ffn_forward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x, int M, int ldx,
                          const uint16_t* residual, int ld_residual, uint16_t* y, int ldy,
-                         uint16_t* gate_up, void* workspace, size_t workspace_bytes, void* stream);
+                         float* gate_up, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Gradients of sum(dy * y) for the block above (the residual's is dy itself):
  *   dh = dy Wd; dg = dh u act'(g); du = dh act(g); h = act(g) u
  *   dx = dg Wg + du Wu; dgate = dg^T x; dup = du^T x; ddown = dy^T h
  * g | u = gate_up from the forward call, the same x and weights.  dg, du and h
- * are rounded to bf16 as operands of the products that follow; every sum is
- * fp32 and every gradient is rounded to bf16 once.  Each of dx [M, hidden],
+ * are rounded to bf16 once as operands of the products that follow; g, u and
+ * every sum are fp32 and every gradient is rounded to bf16 once.  Each of dx [M, hidden],
  * dgate, dup [mlp, hidden], ddown [hidden, mlp] may be NULL (not wanted); the
  * others are overwritten, in the same bits on every call (no atomics).  With
  * M = 0 the weights' gradients are set to 0.  A row of dy, x or gate_up whose
  * values are not finite makes the weights' gradients not finite. */
 int qi_gated_ffn_backward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x, int M, int ldx,
-                          const uint16_t* dy, int ld_dy, const uint16_t* gate_up, uint16_t* dx,
+                          const uint16_t* dy, int ld_dy, const float* gate_up, uint16_t* dx,
                           int ld_dx, uint16_t* dgate, uint16_t* dup, uint16_t* ddown,
                           void* workspace, size_t workspace_bytes, void* stream);
 

@@ -37,6 +37,7 @@ def within(got, ref, tol, what=""):
 
 def same_bits(a, b):
     """Equal bit patterns (NaN equal to itself, unlike torch.equal)."""
+    assert a.dtype == b.dtype
     return torch.equal(a.contiguous().view(torch.int16), b.contiguous().view(torch.int16))
 
 
@@ -425,8 +426,9 @@ def check_forward(ctx, x, wg, wu, wd, act, res=None, **kw):
     X, G, Uw, D = x.double(), wg.double(), wu.double(), wd.double()
     g, u = X @ G.T, X @ Uw.T
     tg, tu = acc_tol(X, G), acc_tol(X, Uw)
-    within(gu[:, :F], g, U * g.abs() + tg + 1e-30, "gate")
-    within(gu[:, F:], u, U * u.abs() + tu + 1e-30, "up")
+    assert gu.dtype == torch.float32
+    within(gu[:, :F], g, tg + 1e-30, "gate")     # kept in fp32: no rounding but the sum's
+    within(gu[:, F:], u, tu + 1e-30, "up")
     a = act64(g, act)
     h = a * u
     th = U * h.abs() + 2.0 ** -16 * h.abs() + tg * u.abs() + tu * a.abs() + tg * tu
@@ -514,6 +516,31 @@ def test_gated_ffn_gradients_against_differences(ctx, act):
         n = max(H, F, M)
         tol = 4 * U * n ** 0.5 * (grad.double() * d).norm().item()
         assert abs(diff - (grad.double() * d).sum().item()) <= tol + 1e-6 * abs(diff)
+
+
+@pytest.mark.parametrize("M,H,F", [(300, 256, 520), (1100, 512, 1384)])
+def test_gated_ffn_gradients_keep_their_precision(ctx, M, H, F):
+    """Relative error (2-norm) of every gradient against 64 bits.  What rounds: the
+    gradient itself, and dg, du or h as an operand; g and u do not.  A rounding to
+    bf16 is off by 2^-8 times a uniform number in (-1, 1) relative to the power of
+    two below the value: 2^-8 / sqrt(3) at 1, half that at 2, and with the values
+    spread over that octave sqrt(1 / ln 16) = 0.60 of it in the mean square,
+    1.36e-3 of the value; at most 2^-8 / sqrt(3) = 2.26e-3 whatever the spread.
+    Two of them in quadrature: 3.19e-3 at most.  g and u rounded too would add
+    two or three more."""
+    x, wg, wu, wd = ffn_case(M, H, F)
+    w = qi.gated_ffn_struct(wg, wu, wd)
+    dy = rand(M, H, seed=9)
+    _, gu = qi.qi_gated_ffn_forward(ctx, w, x, save=True)
+    got = qi.qi_gated_ffn_backward(ctx, w, x, dy, gu)
+    ctx.check()
+    X, G, Uw, D, Y = x.double(), wg.double(), wu.double(), wd.double(), dy.double()
+    g, u = X @ G.T, X @ Uw.T
+    dh = Y @ D
+    dg, du = dh * u * act64_grad(g, qi.QI_ACT_SILU), dh * act64(g, qi.QI_ACT_SILU)
+    refs = (dg @ G + du @ Uw, dg.T @ X, du.T @ X, Y.T @ (act64(g, qi.QI_ACT_SILU) * u))
+    for t, ref in zip(got, refs):
+        assert ((t.double() - ref).norm() / ref.norm()).item() <= 3.19e-3
 
 
 def test_gated_ffn_wanted_gradients_strides_and_zero_rows(ctx):
