@@ -63,8 +63,13 @@ constexpr int AP_OUT = 32 * 64;   // bytes of a softmax warp's staged output: 32
 constexpr int AP_SMEM = 3 * AP_TILE + 8 * AP_OUT + 128;   // Q, K, V, two stages per warp
 static_assert(2 * (AP_SMEM + 1024) <= 233472, "two CTAs per SM");
 
+// A kernel's parameters carry the plan.  Most tables are short, and a launch with
+// 12 KB of parameters takes 1 us longer, so the kernels exist for two sizes.
+using ApFewPlan = PackedTable<16, 64>;
+
+template <class Plan>
 struct ApKernelParams {
-  PackedPlan plan;
+  Plan plan;
   const uint16_t* q;   // for the token kernel (the tile kernel reads it through a tensor map)
   int ldq;
   uint16_t* o;
@@ -84,10 +89,12 @@ struct ApKernelParams {
 struct ApUnit {
   int s, ct, h, j;
 };
-__host__ __device__ __forceinline__ int ap_tiles(const PackedPlan& d, int s) {
+template <class Plan>
+__host__ __device__ __forceinline__ int ap_tiles(const Plan& d, int s) {
   return (d.seq[s].ql + d.P - 1) / d.P;
 }
-__host__ __device__ __forceinline__ ApUnit ap_unit(const PackedPlan& d, int kv_heads, int b) {
+template <class Plan>
+__host__ __device__ __forceinline__ ApUnit ap_unit(const Plan& d, int kv_heads, int b) {
   if (d.n_order > 0) {
     const int i = b / kv_heads;
     ApUnit u;
@@ -116,7 +123,8 @@ __host__ __device__ __forceinline__ ApUnit ap_unit(const PackedPlan& d, int kv_h
   u.j = e % nsp;
   return u;
 }
-__host__ __device__ __forceinline__ int ap_slot(const PackedPlan& d, int kv_heads, int s, int ct, int h, int j) {
+template <class Plan>
+__host__ __device__ __forceinline__ int ap_slot(const Plan& d, int kv_heads, int s, int ct, int h, int j) {
   return d.seq[s].sbase + (ct * d.seq[s].nsp + j) * kv_heads + h;
 }
 
@@ -172,10 +180,11 @@ struct ApWork {
   int lo, n;
   int tail;     // keys of the last of them that some row sees (128: all)
 };
-__device__ __forceinline__ ApWork ap_work(const PackedPlan& d, int kv_heads, int b) {
+template <class Plan>
+__device__ __forceinline__ ApWork ap_work(const Plan& d, int kv_heads, int b) {
   ApWork w;
   w.u = ap_unit(d, kv_heads, b);
-  const PackedPlan::Seq& s = d.seq[w.u.s];
+  const PackedSeq& s = d.seq[w.u.s];
   const int end = max(0, s.kl - s.ql + min((w.u.ct + 1) * d.P, s.ql));   // keys that some row sees
   const int tiles = (end + AP_ROWS - 1) / AP_ROWS;
   w.lo = 0;
@@ -194,7 +203,8 @@ __device__ __forceinline__ ApWork ap_work(const PackedPlan& d, int kv_heads, int
 // divisions, too long to do between two short units).  Warp-collective.
 struct ApList {
   int base, at, ct, lo, n, j;   // at: sequence, head; lo: with the tail
-  __device__ __forceinline__ void fill(const PackedPlan& d, int kv_heads, int from) {
+  template <class Plan>
+  __device__ __forceinline__ void fill(const Plan& d, int kv_heads, int from) {
     base = from;
     const int b = ap_unit_of(from + (threadIdx.x & 31));
     n = -1;   // past the last unit
@@ -209,7 +219,8 @@ struct ApList {
     __syncwarp();
   }
   // n < 0: there is no such round
-  __device__ __forceinline__ ApWork get(const PackedPlan& d, int kv_heads, int round) {
+  template <class Plan>
+  __device__ __forceinline__ ApWork get(const Plan& d, int kv_heads, int round) {
     if (round - base >= 32) fill(d, kv_heads, round);
     const int i = round - base;
     ApWork w;
@@ -224,7 +235,8 @@ struct ApList {
     return w;
   }
   // the next unit with key tiles, from `round` on
-  __device__ __forceinline__ ApWork next(const PackedPlan& d, int kv_heads, int& round) {
+  template <class Plan>
+  __device__ __forceinline__ ApWork next(const Plan& d, int kv_heads, int& round) {
     ApWork w;
     do w = get(d, kv_heads, round++);
     while (w.n == 0);
@@ -233,11 +245,12 @@ struct ApList {
 };
 static_assert(AP_MAX_SEQS <= 256, "sequence in 8 bits");
 
+template <class Plan>
 __global__ void __launch_bounds__(AP_THREADS, 2)
     ap_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-              const __grid_constant__ ApKernelParams p) {
-  const PackedPlan& d = p.plan;
+              const __grid_constant__ ApKernelParams<Plan> p) {
+  const Plan& d = p.plan;
   int* status = p.status;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {   // (two CTAs leave no room to align it by hand)
@@ -408,7 +421,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     for (int round = 0; ok; ++round) {
       const ApWork w = list.get(d, p.kv_heads, round);
       if (w.n < 0) break;
-      const PackedPlan::Seq& sq = d.seq[w.u.s];
+      const PackedSeq& sq = d.seq[w.u.s];
       const int pos = w.u.ct * P + row_pos;           // query position of this row
       const bool live = row < P * G && pos < sq.ql;
       const int lim = live ? max(0, sq.kl - sq.ql + 1 + pos) : 0;   // keys this row sees
@@ -655,10 +668,11 @@ __device__ __forceinline__ bool at_all(bool pred) {
   return r != 0;
 }
 
+template <class Plan>
 __global__ void __launch_bounds__(AT_THREADS, 2)
     ap_token_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                    const __grid_constant__ ApKernelParams p) {
-  const PackedPlan& d = p.plan;
+                    const __grid_constant__ ApKernelParams<Plan> p) {
+  const Plan& d = p.plan;
   int* status = p.status;
   __shared__ float s_ml[AT_WARPS][16][2];
   __shared__ float s_o[AT_WARPS][4][128];
@@ -749,7 +763,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2)
   int i = 0;   // steps taken, over all units
   for (int round = 0; ap_unit_of(round) < total; ++round) {
     if (round > 0) w = work_of(ap_unit_of(round));
-    const PackedPlan::Seq& sq = d.seq[w.u.s];
+    const PackedSeq& sq = d.seq[w.u.s];
     const int ql = sq.ql, kl = sq.kl, nsp = sq.nsp, r0 = w.r0, rows = w.rows;
     if (r0 >= rows) continue;
     uint32_t qa[8][4];   // A fragments of 16 head columns each
@@ -922,8 +936,9 @@ __global__ void __launch_bounds__(AT_THREADS, 2)
 // same order.  One CTA per row: warp w adds ranges w, w + 4, ..., 32 lanes
 // cover the 128 columns, and the four sums are added in shared memory.
 constexpr int AP_JOIN_WARPS = 4;
-__global__ void __launch_bounds__(32 * AP_JOIN_WARPS) ap_join_kernel(const __grid_constant__ ApKernelParams p) {
-  const PackedPlan& d = p.plan;
+template <class Plan>
+__global__ void __launch_bounds__(32 * AP_JOIN_WARPS) ap_join_kernel(const __grid_constant__ ApKernelParams<Plan> p) {
+  const Plan& d = p.plan;
   __shared__ float4 s_o[AP_JOIN_WARPS][32];
   __shared__ float s_l[AP_JOIN_WARPS];
   const int b = static_cast<int>(blockIdx.x), r = static_cast<int>(blockIdx.y);
@@ -1031,8 +1046,7 @@ static void plan_finish(std::vector<PlanSeq>& seq, int kv_heads, PackedPlan* d) 
 
 void packed_plan(const int32_t* spans, int n, int heads, int kv_heads, int num_sms, PackedPlan* tile,
                  PackedPlan* token) {
-  memset(tile, 0, sizeof(*tile));
-  memset(token, 0, sizeof(*token));
+  for (PackedPlan* d : {tile, token}) d->n_seqs = d->units = d->slots = d->slot_rows = d->groups = d->n_order = 0;
   tile->G = token->G = heads / kv_heads;
   tile->P = token->P = AP_ROWS / tile->G;
   std::vector<PlanSeq> big, few;
@@ -1111,77 +1125,114 @@ static bool allow_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
   return true;
 }
 
-static int launch_join(const ApKernelParams& p, cudaStream_t st) {
+template <class Plan>
+static int launch_join(const ApKernelParams<Plan>& p, cudaStream_t st) {
   if (p.plan.groups == 0) return 0;
-  launch_pdl(ap_join_kernel, dim3(p.plan.groups, p.plan.slot_rows), dim3(32 * AP_JOIN_WARPS), 0, st, 1, p);
+  launch_pdl(ap_join_kernel<Plan>, dim3(p.plan.groups, p.plan.slot_rows), dim3(32 * AP_JOIN_WARPS), 0, st, 1, p);
   return launch_result();
+}
+
+// The parameters that both kernels take, with the plan's partial results from `scratch`.
+template <class Plan>
+static void ap_params(const PackedAttnParams& a, const PackedPlan& d, uint8_t* scratch, ApKernelParams<Plan>* p) {
+  Plan& t = p->plan;
+  t.n_seqs = d.n_seqs;
+  t.G = d.G;
+  t.P = d.P;
+  t.units = d.units;
+  t.slots = d.slots;
+  t.slot_rows = d.slot_rows;
+  t.groups = d.groups;
+  t.n_order = d.n_order;
+  memcpy(t.seq, d.seq, sizeof(PackedSeq) * static_cast<size_t>(d.n_seqs));
+  memcpy(t.order, d.order, sizeof(uint32_t) * static_cast<size_t>(d.n_order));
+  p->q = a.q;
+  p->ldq = a.ldq;
+  p->o = a.o;
+  p->ldo = a.ldo;
+  p->kv_heads = a.kv_heads;
+  p->tma_out = 0;
+  p->row_blocks = 0;
+  p->sm_scale = a.sm_scale;
+  p->status = a.status;
+  p->part_o = reinterpret_cast<float*>(scratch);
+  p->part_ml = p->part_o + static_cast<size_t>(d.slots) * d.slot_rows * 128;
+}
+
+// K and V maps; without any key row nothing is loaded and they lie over q.
+static bool ap_kv_maps(const PackedAttnParams& a, CUtensorMap* tk, CUtensorMap* tv, uint32_t keys) {
+  const bool none = a.k_rows == 0;
+  const uint64_t width = static_cast<uint64_t>(a.kv_heads) * 128, n = none ? a.q_rows : a.k_rows;
+  return make_tmap_2d(tk, none ? a.q : a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, width, n,
+                      static_cast<uint64_t>(none ? a.ldq : a.ldk) * 2, 64, keys) &&
+         make_tmap_2d(tv, none ? a.q : a.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, width, n,
+                      static_cast<uint64_t>(none ? a.ldq : a.ldv) * 2, 64, keys);
+}
+
+template <class Plan>
+static int launch_tile(const PackedAttnParams& a, const PackedPlan& d, uint8_t* scratch, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(ap_kernel<Plan>, AP_SMEM, done)) {
+    launch_result();
+    return -1;
+  }
+  ApKernelParams<Plan> p;
+  ap_params(a, d, scratch, &p);
+  CUtensorMap tq, tk, tv, to;
+  if (!make_tmap_rows3(&tq, a.q, 128, a.heads, a.q_rows, static_cast<uint64_t>(a.ldq) * 2, 64, d.G, d.P) ||
+      !ap_kv_maps(a, &tk, &tv, AP_ROWS))
+    return -2;
+  // output boxes: the 32 rows of a softmax warp, min(G, 32) heads x 32 / G positions
+  p.tma_out = 32 % d.G == 0 || d.G % 32 == 0;
+  const uint32_t box_heads = d.G < 32 ? d.G : 32;
+  if (!p.tma_out) to = tq;
+  else if (!make_tmap_rows3(&to, a.o, 128, a.heads, a.q_rows, static_cast<uint64_t>(a.ldo) * 2, 32, box_heads,
+                            32 / box_heads))
+    return -2;
+  launch_pdl(ap_kernel<Plan>, dim3(std::min(d.units, 2 * a.num_sms)), dim3(AP_THREADS), AP_SMEM, st, 1, tq, tk, tv, to,
+             p);
+  return launch_result() || launch_join(p, st) ? -1 : 0;
+}
+
+template <class Plan>
+static int launch_token(const PackedAttnParams& a, const PackedPlan& d, uint8_t* scratch, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(ap_token_kernel<Plan>, AT_SMEM, done)) {
+    launch_result();
+    return -1;
+  }
+  ApKernelParams<Plan> p;
+  ap_params(a, d, scratch, &p);
+  int rows = 0;
+  for (int i = 0; i < d.n_seqs; ++i) rows = std::max(rows, d.seq[i].ql * d.G);
+  p.row_blocks = (rows + 15) / 16;
+  CUtensorMap tk, tv;
+  if (!ap_kv_maps(a, &tk, &tv, AT_KEYS)) return -2;
+  const long long total = static_cast<long long>(d.units) * p.row_blocks;
+  const int grid = static_cast<int>(std::min<long long>(total, 2ll * a.num_sms));
+  launch_pdl(ap_token_kernel<Plan>, dim3(grid), dim3(AT_THREADS), AT_SMEM, st, 1, tk, tv, p);
+  return launch_result() || launch_join(p, st) ? -1 : 0;
+}
+
+template <class Plan>
+static bool ap_holds(const PackedPlan& d) {
+  return d.n_seqs <= static_cast<int>(sizeof(Plan::seq) / sizeof(PackedSeq)) &&
+         d.n_order <= static_cast<int>(sizeof(Plan::order) / sizeof(uint32_t));
 }
 
 int launch_attention_packed(const PackedAttnParams& a, const PackedPlan& tile, const PackedPlan& token,
                             cudaStream_t st) {
-  ApKernelParams p;
-  p.q = a.q;
-  p.ldq = a.ldq;
-  p.o = a.o;
-  p.ldo = a.ldo;
-  p.kv_heads = a.kv_heads;
-  p.sm_scale = a.sm_scale;
-  p.status = a.status;
   uint8_t* scratch = static_cast<uint8_t*>(a.scratch);
-  auto partials = [&](const PackedPlan& d, size_t at) {
-    p.plan = d;
-    p.part_o = reinterpret_cast<float*>(scratch + at);
-    p.part_ml = p.part_o + static_cast<size_t>(d.slots) * d.slot_rows * 128;
-  };
-  // K and V maps; without any key row nothing is loaded and they lie over q
-  auto kv_maps = [&](CUtensorMap* tk, CUtensorMap* tv, uint32_t keys) {
-    const bool none = a.k_rows == 0;
-    const uint64_t width = static_cast<uint64_t>(a.kv_heads) * 128, n = none ? a.q_rows : a.k_rows;
-    return make_tmap_2d(tk, none ? a.q : a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, width, n,
-                        static_cast<uint64_t>(none ? a.ldq : a.ldk) * 2, 64, keys) &&
-           make_tmap_2d(tv, none ? a.q : a.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, width, n,
-                        static_cast<uint64_t>(none ? a.ldq : a.ldv) * 2, 64, keys);
-  };
-  if (tile.units > 0) {
-    static std::atomic<uint64_t> done{0};
-    if (!allow_smem(ap_kernel, AP_SMEM, done)) {
-      launch_result();
-      return -1;
-    }
-    CUtensorMap tq, tk, tv;
-    if (!make_tmap_rows3(&tq, a.q, 128, a.heads, a.q_rows, static_cast<uint64_t>(a.ldq) * 2, 64, tile.G, tile.P) ||
-        !kv_maps(&tk, &tv, AP_ROWS))
-      return -2;
-    // output boxes: the 32 rows of a softmax warp, min(G, 32) heads x 32 / G positions
-    CUtensorMap to;
-    p.tma_out = 32 % tile.G == 0 || tile.G % 32 == 0;
-    const uint32_t box_heads = tile.G < 32 ? tile.G : 32;
-    if (!p.tma_out) to = tq;
-    else if (!make_tmap_rows3(&to, a.o, 128, a.heads, a.q_rows, static_cast<uint64_t>(a.ldo) * 2, 32, box_heads,
-                              32 / box_heads))
-      return -2;
-    partials(tile, 0);
-    launch_pdl(ap_kernel, dim3(std::min(tile.units, 2 * a.num_sms)), dim3(AP_THREADS), AP_SMEM, st, 1, tq, tk, tv, to, p);
-    if (launch_result() || launch_join(p, st)) return -1;
+  int r = 0;
+  if (tile.units > 0)
+    r = ap_holds<ApFewPlan>(tile) ? launch_tile<ApFewPlan>(a, tile, scratch, st)
+                                  : launch_tile<PackedPlan>(a, tile, scratch, st);
+  if (r == 0 && token.units > 0) {
+    scratch += packed_plan_bytes(tile);
+    r = ap_holds<ApFewPlan>(token) ? launch_token<ApFewPlan>(a, token, scratch, st)
+                                   : launch_token<PackedPlan>(a, token, scratch, st);
   }
-  if (token.units > 0) {
-    int rows = 0;
-    for (int i = 0; i < token.n_seqs; ++i) rows = std::max(rows, token.seq[i].ql * token.G);
-    static std::atomic<uint64_t> done{0};
-    if (!allow_smem(ap_token_kernel, AT_SMEM, done)) {
-      launch_result();
-      return -1;
-    }
-    CUtensorMap tk, tv;
-    if (!kv_maps(&tk, &tv, AT_KEYS)) return -2;
-    partials(token, packed_plan_bytes(tile));
-    p.row_blocks = (rows + 15) / 16;
-    const long long total = static_cast<long long>(token.units) * p.row_blocks;
-    const int grid = static_cast<int>(std::min<long long>(total, 2ll * a.num_sms));
-    launch_pdl(ap_token_kernel, dim3(grid), dim3(AT_THREADS), AT_SMEM, st, 1, tk, tv, p);
-    if (launch_result() || launch_join(p, st)) return -1;
-  }
-  return 0;
+  return r;
 }
 
 }  // namespace qi

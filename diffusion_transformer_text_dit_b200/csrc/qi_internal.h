@@ -339,25 +339,28 @@ int launch_gated_dw(const GatedBackwardParams& p, cudaStream_t st);        // th
 // Causal attention over packed sequences with grouped heads (qi_attn_causal_packed).
 constexpr int AP_MAX_SEQS = 256;
 constexpr int AP_MAX_ORDER = 1024;
-struct PackedPlan {
+struct PackedSeq {        // in launch order
+  int q0, ql, k0, kl;
+  int nsp;                // key-range splits of each of the sequence's query tiles
+  int ustart;             // first unit of the levels that sequences 0..i share
+  int sbase;              // first partial result, if split
+  int cbase;              // first group of the joining kernel, if split
+};
+template <int SEQS, int ORDER>
+struct PackedTable {
   int n_seqs;             // sequences with queries
   int G, P;               // query heads per key/value head; query positions per 128-row tile
   int units;              // units of work (query tile, key/value head, key range)
   int slots;              // partial results (0: no sequence is split over its keys)
   int slot_rows;          // rows of one partial result
   int groups;             // split (query tile, key/value head)s
-  struct Seq {            // in launch order
-    int q0, ql, k0, kl;
-    int nsp;              // key-range splits of each of the sequence's query tiles
-    int ustart;           // first unit of the levels that sequences 0..i share
-    int sbase;            // first partial result, if split
-    int cbase;            // first group of the joining kernel, if split
-  } seq[AP_MAX_SEQS];
   // units of one key/value head in launch order (sequence << 24 | query tile), if none is split
   // and there are few enough; else n_order is 0 and the order follows from ustart
   int n_order;
-  uint32_t order[AP_MAX_ORDER];
+  PackedSeq seq[SEQS];
+  uint32_t order[ORDER];
 };
+using PackedPlan = PackedTable<AP_MAX_SEQS, AP_MAX_ORDER>;
 struct PackedAttnParams {
   const uint16_t* q;
   const uint16_t* k;

@@ -586,13 +586,16 @@ def qi_attn_causal_packed(ctx: Context, q, k, v, spans: torch.Tensor, heads: int
     kp, ldk = _rows(ctx, k, "k", KW)
     vp, ldv = _rows(ctx, v, "v", KW)
     op, ldo = _rows(ctx, o, "o", W)
+    L, table, n_seqs = lib(), _spans(spans), spans.shape[0]
     if workspace is None:
-        n = qi_attn_causal_packed_workspace_bytes(ctx, spans, heads, kv_heads)
+        size = C.c_size_t()
+        check(L.qi_attn_causal_packed_workspace_bytes(ctx.handle, table, n_seqs, heads, kv_heads, C.byref(size)))
+        n = size.value
         if n:
             workspace = _new(n, q, stream, torch.uint8)
-    check(lib().qi_attn_causal_packed(
+    check(L.qi_attn_causal_packed(
         ctx.handle, qp, ldq, q.shape[0], kp, ldk, vp, ldv, k.shape[0], heads, kv_heads, 128,
-        _spans(spans), spans.shape[0], sm_scale if sm_scale is not None else 128 ** -0.5, op, ldo,
+        table, n_seqs, sm_scale if sm_scale is not None else 128 ** -0.5, op, ldo,
         *_scratch(workspace, q), st))
     return o
 
