@@ -10,26 +10,32 @@
 //
 // Layout of the work.  The G = heads / kv_heads query heads that share a
 // key/value head are packed into the rows of one 128-row tile: row r of a
-// tile is head r mod G at query position p0 + r / G, so one 128-key tile of K
-// and V serves all of them and a short prompt still fills its tiles.  A tile
+// tile is head r mod G at query position p0 + r / G, so one load of K and V
+// serves all of them and a short prompt still fills its tiles.  A tile
 // holds P = 128 / G positions; rows past P G and past the sequence's last
 // query are computed and dropped.  Two CTAs share an SM.
 //
-// Per 128-key tile: S = Q K^T (both operands in shared memory), one thread per
-// row takes the softmax, writes P as bf16 over S, and O += P V reads P from
-// TMEM (256 columns a CTA: S | O).  P is rounded to bf16 for the tensor core;
-// the row sum adds the unrounded fp32 values.  PV(j) and S(j + 1) are issued
-// together, and one commit tells that both are complete, that the K and V
-// tiles may be replaced (one stage each: a load has the whole softmax of a
-// tile to arrive) and that S(j + 1) can be read.  What bounds a CTA is that
-// chain, softmax - PV - S - softmax; the two CTAs of an SM fill each other's
-// gaps.  A CTA runs through several query tiles: S of the next one's first
-// key tile follows the last PV of this one, so its loads and its MMA lie under
-// the last softmax and the division and store of O.
+// Keys come in steps of 64.  S = Q K^T (both operands in shared memory), one
+// thread per row takes the softmax, writes P as bf16 over S, and O += P V reads
+// P from TMEM.  P is rounded to bf16 for the tensor core; the row sum adds the
+// unrounded fp32 values.  A CTA's 256 TMEM columns are two slots for S and P
+// and O, so S of the next step is there when a softmax ends, and the tensor
+// core works through P V (i), S (i + 2) of one slot under the softmax of the
+// other; K and V have two stages each, and S of the next query tile's first
+// steps follows while this one's last softmax runs and O is divided and stored.
+// (Steps of 128 keys leave room for one S, so that every softmax waits for P V
+// and S, and compute more that the causal cut drops: 24 ragged prompts, 8500
+// tokens, 59 us against 52.5; 32 prompts of 128 tokens 23 against 21.4; 4096
+// tokens the same 135.)
 //
-// The last key tile is cut to the keys that some row sees (in steps of 16 for the MMAs, 32 for the softmax).
+// What bounds it: the base-2 exponentials (16 a clock per SM) and the tensor
+// core are each busy half the time, between the dependent steps of four softmax
+// warps per CTA.  16384 tokens take 1.98 ms, 1.11 PFLOP/s, at 1.8 GHz; over
+// seconds the power limit holds the clock at 1.62 GHz (2.29 ms).
 //
-// Rows that a sequence does not own: the last key tile may reach into the
+// The last step is cut to the keys that some row sees (in steps of 16 for the MMAs, 32 for the softmax).
+//
+// Rows that a sequence does not own: the last step may reach into the
 // next sequence or into rows of a cache that were never written.  Their
 // scores are masked, and their V rows, whose weight is 0 but whose values may
 // be infinite or NaN, are kept out of the product: P V runs over the 16-key
@@ -57,10 +63,13 @@ namespace qi {
 
 constexpr int AP_ROWS = 128;
 constexpr int AP_THREADS = 192;   // 4 softmax warps, TMA, MMA
+constexpr int AP_KEYS = 64;        // keys of a step
 constexpr int AP_TILE = 128 * 128 * 2;
-constexpr int AP_HALF = 128 * 128;
+constexpr int AP_HALF = 128 * 128;          // bytes of 64 columns of the Q tile
+constexpr int AP_STEP = AP_KEYS * 128 * 2;  // bytes of K or V of a step
+constexpr int AP_STEP_HALF = AP_KEYS * 128;
 constexpr int AP_OUT = 32 * 64;   // bytes of a softmax warp's staged output: 32 rows x 32 columns
-constexpr int AP_SMEM = 3 * AP_TILE + 8 * AP_OUT + 128;   // Q, K, V, two stages per warp
+constexpr int AP_SMEM = AP_TILE + 4 * AP_STEP + 8 * AP_OUT + 128 + 512;   // Q, two stages of K and V, two of O per warp
 static_assert(2 * (AP_SMEM + 1024) <= 233472, "two CTAs per SM");
 
 // A kernel's parameters carry the plan.  Most tables are short, and a launch with
@@ -168,17 +177,30 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
+// Whether a phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_done(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // One arrival for the warp, after what all its lanes did before.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
 }
 
-// A unit of the tile kernel: a query tile over key tiles [lo, lo + n).
+// A unit of the tile kernel: a query tile over steps [lo, lo + n) of the keys.
 struct ApWork {
   ApUnit u;
   int lo, n;
-  int tail;     // keys of the last of them that some row sees (128: all)
+  int tail;     // keys of the last of them that some row sees (AP_KEYS: all)
 };
 template <class Plan>
 __device__ __forceinline__ ApWork ap_work(const Plan& d, int kv_heads, int b) {
@@ -186,64 +208,97 @@ __device__ __forceinline__ ApWork ap_work(const Plan& d, int kv_heads, int b) {
   w.u = ap_unit(d, kv_heads, b);
   const PackedSeq& s = d.seq[w.u.s];
   const int end = max(0, s.kl - s.ql + min((w.u.ct + 1) * d.P, s.ql));   // keys that some row sees
-  const int tiles = (end + AP_ROWS - 1) / AP_ROWS;
+  const int steps = (end + AP_KEYS - 1) / AP_KEYS;
   w.lo = 0;
-  int hi = tiles;
+  int hi = steps;
   if (s.nsp > 1) {
-    w.lo = static_cast<int>(static_cast<long long>(tiles) * w.u.j / s.nsp);
-    hi = static_cast<int>(static_cast<long long>(tiles) * (w.u.j + 1) / s.nsp);
+    w.lo = static_cast<int>(static_cast<long long>(steps) * w.u.j / s.nsp);
+    hi = static_cast<int>(static_cast<long long>(steps) * (w.u.j + 1) / s.nsp);
   }
   w.n = hi - w.lo;
-  w.tail = w.n > 0 && hi == tiles ? end - (tiles - 1) * AP_ROWS : AP_ROWS;
+  w.tail = w.n > 0 && hi == steps ? end - (steps - 1) * AP_KEYS : AP_KEYS;
+  if (w.n == 0) {   // no keys: one step that is masked throughout
+    w.n = 1;
+    w.tail = 0;
+  }
   return w;
 }
 
-// The units of a CTA, decoded 32 at a time: lane i of a warp holds round
-// base + i, and a lookup is a shuffle (a decode is a search and several
-// divisions, too long to do between two short units).  Warp-collective.
-struct ApList {
-  int base, at, ct, lo, n, j;   // at: sequence, head; lo: with the tail
-  template <class Plan>
-  __device__ __forceinline__ void fill(const Plan& d, int kv_heads, int from) {
-    base = from;
-    const int b = ap_unit_of(from + (threadIdx.x & 31));
-    n = -1;   // past the last unit
-    if (b < d.units) {
-      const ApWork w = ap_work(d, kv_heads, b);
-      at = w.u.s | (w.u.h << 8);             // s < 256
-      ct = w.u.ct;
-      lo = w.lo | ((w.tail - 1) << 24);      // tiles below 2^24, tail 1..128
-      n = w.n;
-      j = w.u.j;
-    }
-    __syncwarp();
-  }
-  // n < 0: there is no such round
-  template <class Plan>
-  __device__ __forceinline__ ApWork get(const Plan& d, int kv_heads, int round) {
-    if (round - base >= 32) fill(d, kv_heads, round);
-    const int i = round - base;
-    ApWork w;
-    const int a = __shfl_sync(0xffffffffu, at, i), l = __shfl_sync(0xffffffffu, lo, i);
-    w.u.ct = __shfl_sync(0xffffffffu, ct, i);
-    w.n = __shfl_sync(0xffffffffu, n, i);
-    w.u.j = __shfl_sync(0xffffffffu, j, i);
-    w.u.s = a & 255;
-    w.u.h = a >> 8;
-    w.lo = l & 0xFFFFFF;
-    w.tail = (l >> 24) + 1;
-    return w;
-  }
-  // the next unit with key tiles, from `round` on
-  template <class Plan>
-  __device__ __forceinline__ ApWork next(const Plan& d, int kv_heads, int& round) {
-    ApWork w;
-    do w = get(d, kv_heads, round++);
-    while (w.n == 0);
-    return w;
-  }
+// The units of a CTA.  The grid has one CTA per unit, longest first; a running
+// CTA takes the next one that has not started from the hardware (cluster launch
+// control: it is cancelled and its number handed over), so that SMs which are
+// done early go on.  The producer warp asks shortly before a unit's last loads
+// (earlier, and long units would be handed to CTAs that still have long ones
+// to finish), decodes the answer and puts it into a ring that every warp reads.  (A unit's reading warps are never
+// further apart than the ring is long: a step's S, and so the loads behind it,
+// waits for the P V two steps before.)
+constexpr int AP_RING = 8;
+constexpr int AP_AHEAD = 4;   // steps before the end of a unit's loads at which the next unit is asked for
+struct ApRing {
+  int4 unit[AP_RING];       // sequence | head << 8, query tile, steps (-1: behind the last), key split
+  int2 range[AP_RING];      // first step, keys of the last
+  uint4 answer;             // of the launch control
+  uint64_t full[AP_RING], empty[AP_RING], asked;
 };
 static_assert(AP_MAX_SEQS <= 256, "sequence in 8 bits");
+constexpr int AP_READERS = 5;   // the softmax warps and the MMA warp; the producer keeps its own order
+
+__device__ __forceinline__ void ap_ask(ApRing* r) {
+  mbar_expect_elect(&r->asked, 16);
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];\n\t}" ::"r"(
+          smem_u32(&r->answer)),
+      "r"(smem_u32(&r->asked))
+      : "memory");
+}
+// The CTA that was handed over, or -1.
+__device__ __forceinline__ int ap_answer(ApRing* r) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t"
+      "ld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_u32(&r->answer))
+      : "memory");
+  return got ? static_cast<int>(x) : -1;
+}
+
+// Unit k of the CTA into its place of the ring.
+__device__ __forceinline__ void ap_publish(ApRing* r, int k, const ApWork& w, int lane) {
+  if (lane == 0) {
+    r->unit[k % AP_RING] = make_int4(w.u.s | (w.u.h << 8), w.u.ct, w.n, w.u.j);
+    r->range[k % AP_RING] = make_int2(w.lo, w.tail);
+  }
+  warp_arrive(&r->full[k % AP_RING], lane);
+}
+// Unit k of the CTA, once it is in the ring (every lane gets it).
+__device__ __forceinline__ bool ap_read(ApRing* r, int k, ApWork* w, int* status) {
+  if (!mbar_wait_warp(&r->full[k % AP_RING], (k / AP_RING) & 1, status)) return false;
+  const int4 u = r->unit[k % AP_RING];
+  const int2 t = r->range[k % AP_RING];
+  w->u.s = u.x & 255;
+  w->u.h = u.x >> 8;
+  w->u.ct = u.y;
+  w->n = u.z;
+  w->u.j = u.w;
+  w->lo = t.x;
+  w->tail = t.y;
+  return true;
+}
+
+// A place in the sequence of steps that a CTA's units make up; w.n < 0 behind
+// the last (and after a wait that ran out).
+struct ApCursor {
+  ApWork w;
+  int k, j;    // unit of the CTA, step of the unit
+  __device__ __forceinline__ bool live() const { return w.n >= 0; }
+};
 
 template <class Plan>
 __global__ void __launch_bounds__(AP_THREADS, 2)
@@ -258,27 +313,37 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     return;
   }
   uint8_t* sQ = smem;
-  uint8_t* sK = smem + AP_TILE;
-  uint8_t* sV = smem + 2 * AP_TILE;
-  uint8_t* sO = smem + 3 * AP_TILE;   // [4 warps][2][AP_OUT]
+  uint8_t* sK = smem + AP_TILE;          // [2][AP_STEP]
+  uint8_t* sV = sK + 2 * AP_STEP;        // [2][AP_STEP]
+  uint8_t* sO = sV + 2 * AP_STEP;        // [4 warps][2][AP_OUT]
+  // step i uses stage, slot and barriers i & 1, their phase is i >> 1
   uint64_t* q_full = reinterpret_cast<uint64_t*>(sO + 8 * AP_OUT);
-  uint64_t* k_full = q_full + 1;
-  uint64_t* v_full = q_full + 2;
-  uint64_t* s_full = q_full + 3;   // S of a tile and P V of the tile before complete
-  uint64_t* p_full = q_full + 4;
-  uint64_t* o_full = q_full + 5;   // the last P V of a unit complete
-  uint64_t* drain = q_full + 6;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 7);
+  uint64_t* k_full = q_full + 1;   // [2]
+  uint64_t* v_full = q_full + 3;   // [2]
+  uint64_t* s_full = q_full + 5;   // [2] S complete
+  uint64_t* p_full = q_full + 7;   // [2] P written
+  uint64_t* pv_full = q_full + 9;  // [2] P V complete
+  uint64_t* drain = q_full + 11;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 12);
+  ApRing* ring = reinterpret_cast<ApRing*>(q_full + 16);
+  static_assert(sizeof(ApRing) <= 512, "shared memory");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    mbar_init(k_full, 1);
-    mbar_init(v_full, 1);
-    mbar_init(s_full, 1);
-    mbar_init(p_full, 4);
-    mbar_init(o_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_full[i], 1);
+    }
     mbar_init(drain, 1);
+    for (int i = 0; i < AP_RING; ++i) {
+      mbar_init(&ring->full[i], 1);
+      mbar_init(&ring->empty[i], AP_READERS);
+    }
+    mbar_init(&ring->asked, 1);
     fence_mbar_init();
   }
   if (warp == 4 && lane == 0) {
@@ -296,65 +361,99 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  // every role walks the same list of units, decoded from the launch's arguments alone
-  ApList list;
-  list.fill(d, p.kv_heads, 0);
+  if (warp == 4) {   // the first unit, from the launch's arguments alone
+    ap_publish(ring, 0, ap_work(d, p.kv_heads, static_cast<int>(blockIdx.x)), lane);
+  }
   pdl_wait();
   pdl_trigger();
 
   if (warp == 4) {
     // ------------------------------------------------------------ TMA producer (the whole warp, one lane issues)
     bool ok = true;
-    int round = 0, t = 0, units = 0;   // t: key tiles of the units before this one
-    const uint32_t q_bar = smem_u32(q_full), k_bar = smem_u32(k_full), v_bar = smem_u32(v_full);
-    ApWork w = list.next(d, p.kv_heads, round);
+    int units = 0, nk = 0, nv = 0;   // loads of Q, K and V asked for
+    int known = 1;                   // units in the ring
+    int asked = 0, answered = 0;     // questions to the launch control
+    auto take = [&] {   // the answer into the ring
+      if (!mbar_wait_warp(&ring->asked, answered & 1, status)) { ok = false; return; }
+      ++answered;
+      const int b = ap_answer(ring);
+      fence_proxy_async_smem();   // read before it is written again
+      __syncwarp();
+      if (known >= AP_RING &&
+          !mbar_wait_warp(&ring->empty[known % AP_RING], (known / AP_RING - 1) & 1, status)) {
+        ok = false;
+        return;
+      }
+      ApWork w{};
+      w.n = -1;
+      if (b >= 0) w = ap_work(d, p.kv_heads, b);
+      ap_publish(ring, known++, w, lane);
+    };
+    auto unit = [&](ApCursor& c) {   // unit c.k, step 0
+      c.j = 0;
+      if (ok && c.k == known) take();
+      if (!ok || !ap_read(ring, c.k, &c.w, status)) {
+        ok = false;
+        c.w.n = -1;
+      }
+    };
+    auto advance = [&](ApCursor& c) {
+      if (++c.j < c.w.n) return;
+      ++c.k;
+      unit(c);
+    };
+    ApCursor at{{}, 0, 0};     // the step whose S is waited for; K and V cursors run ahead
+    unit(at);
+    ApCursor kc = at, vc = at;
     auto load_q = [&](const ApWork& x) {
       // a box holds P positions x G heads x 64 head columns: rows in tile order
       mbar_expect_elect(q_full, static_cast<uint32_t>(P * G) * 128 * 2);
       for (int half = 0; half < 2; ++half)
-        tma_load_3d_elect(&tmQ, q_bar, sQ + half * AP_HALF, 64 * half, x.u.h * G, d.seq[x.u.s].q0 + x.u.ct * P);
+        tma_load_3d_elect(&tmQ, smem_u32(q_full), sQ + half * AP_HALF, 64 * half, x.u.h * G,
+                          d.seq[x.u.s].q0 + x.u.ct * P);
       ++units;
     };
-    auto load = [&](const CUtensorMap* map, uint64_t* full, uint32_t bar, uint8_t* dst, const ApWork& x, int j) {
-      mbar_expect_elect(full, AP_TILE);
-      for (int half = 0; half < 2; ++half)
-        tma_load_2d_elect<false>(map, bar, dst + half * AP_HALF, x.u.h * 128 + 64 * half,
-                                 d.seq[x.u.s].k0 + (x.lo + j) * AP_ROWS);
-    };
-    int nk = 0, nv = 0;   // K and V tiles asked for
-    if (w.n >= 0) {
-      load_q(w);
-      load(&tmK, k_full, k_bar, sK, w, 0);
-      load(&tmV, v_full, v_bar, sV, w, 0);
-      nk = nv = 1;
-    }
-    while (ok && w.n >= 0) {
-      const ApWork nx = list.next(d, p.kv_heads, round);
-      for (int j = 0; j < w.n; ++j) {
-        if (j + 1 == w.n && nx.n < 0 && nv == t + w.n) break;   // everything is on its way
-        // S of tile t + j and P V of the one before complete: Q (after a unit's last S), K of
-        // this tile and V of the one before have been used
-        if (!mbar_wait_warp(s_full, (t + j) & 1, status)) { ok = false; break; }
-        if (t + j > 0) { load(&tmV, v_full, v_bar, sV, w, j); ++nv; }
-        if (j + 1 < w.n) {
-          load(&tmK, k_full, k_bar, sK, w, j + 1);
-          ++nk;
-        } else if (nx.n >= 0) {
-          load_q(nx);
-          load(&tmK, k_full, k_bar, sK, nx, 0);
-          ++nk;
-        }
+    auto load = [&](const CUtensorMap* map, uint64_t* full, uint8_t* dst, ApCursor& c, int& n) {
+      if (!c.live()) return;
+      if (map == &tmK && asked == answered && c.k + 1 == known && c.w.n - c.j <= AP_AHEAD) {
+        ap_ask(ring);
+        ++asked;
       }
-      t += w.n;
-      w = nx;
+      const int st = n++ & 1;
+      mbar_expect_elect(&full[st], AP_STEP);
+      for (int half = 0; half < 2; ++half)
+        tma_load_2d_elect<false>(map, smem_u32(&full[st]), dst + st * AP_STEP + half * AP_STEP_HALF,
+                                 c.w.u.h * 128 + 64 * half, d.seq[c.w.u.s].k0 + (c.w.lo + c.j) * AP_KEYS);
+      advance(c);
+    };
+    if (at.live()) load_q(at.w);
+    for (int i = 0; i < 2; ++i) {
+      load(&tmK, k_full, sK, kc, nk);
+      load(&tmV, v_full, sV, vc, nv);
     }
-    if (!ok) {   // bounded drain of the loads already armed
-      uint64_t* bars[3] = {q_full, k_full, v_full};
-      const int count[3] = {units, nk, nv};
-      for (int i = 0; i < 3; ++i) {
+    for (int i = 0; ok && at.live(); ++i) {
+      // S(i) complete: its K stage is free, and Q after a unit's last S
+      if (!mbar_wait_warp(&s_full[i & 1], (i >> 1) & 1, status)) { ok = false; break; }
+      const bool last = at.j + 1 == at.w.n;
+      advance(at);
+      if (last && at.live()) load_q(at.w);
+      load(&tmK, k_full, sK, kc, nk);
+      if (i > 0 && vc.live()) {   // P V(i - 1) complete: its V stage is free
+        if (!mbar_wait_warp(&pv_full[(i - 1) & 1], ((i - 1) >> 1) & 1, status)) { ok = false; break; }
+        load(&tmV, v_full, sV, vc, nv);
+      }
+    }
+    if (!ok) {   // bounded drain of what is on its way: the answer, the loads already armed
+      auto landed = [&](uint64_t* bar, int n) {   // n phases
         const uint64_t t0 = globaltimer_ns();
-        while (count[i] > 0 && !mbar_try_wait(bars[i], (count[i] - 1) & 1) && globaltimer_ns() - t0 < QI_WAIT_NS) {
+        while (n > 0 && !mbar_try_wait(bar, (n - 1) & 1) && globaltimer_ns() - t0 < QI_WAIT_NS) {
         }
+      };
+      landed(&ring->asked, asked);
+      landed(q_full, units);
+      for (int st = 0; st < 2; ++st) {
+        landed(&k_full[st], (nk + 1 - st) / 2);
+        landed(&v_full[st], (nv + 1 - st) / 2);
       }
     }
   } else if (warp == 5) {
@@ -362,46 +461,63 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     constexpr uint32_t idesc_m = umma_idesc(false, 128, 0);
     constexpr uint32_t idesc_pv = umma_idesc(false, 128, 128) | (1u << 16);   // B MN-major
     const uint64_t qd = umma_desc_kmajor_sw128(smem_u32(sQ)), kd = umma_desc_kmajor_sw128(smem_u32(sK));
-    const uint64_t vd = umma_desc_mnmajor_sw128(smem_u32(sV), AP_HALF);
+    const uint64_t vd = umma_desc_mnmajor_sw128(smem_u32(sV), AP_STEP_HALF);
     bool ok = true;
-    int round = 0, t = 0, units = 0;
-    auto issue_s = [&](const ApWork& x, int j, int ti) -> bool {
-      if ((j == 0 && !mbar_wait_warp(q_full, units & 1, status)) || !mbar_wait_warp(k_full, ti & 1, status)) return false;
-      if (j == 0) ++units;
-      tc_fence_after();
-      const uint32_t cols = j == x.n - 1 ? static_cast<uint32_t>(x.tail + 15) / 16 * 16 : 128u;
-      const uint32_t idesc = idesc_m | ((cols >> 3) << 17);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const uint64_t off = static_cast<uint64_t>((kk >> 2) * AP_HALF + (kk & 3) * 32) >> 4;
-        umma_f16_elect<false>(tmem_base, qd + off, kd + off, idesc, kk > 0);
+    int x = 0, i = 0, units = 0;   // next S, next P V, units whose Q has been used
+    auto unit = [&](ApCursor& c, bool release) {
+      c.j = 0;
+      if (!ap_read(ring, c.k, &c.w, status)) {
+        ok = false;
+        c.w.n = -1;
+      } else if (release) {
+        warp_arrive(&ring->empty[c.k % AP_RING], lane);
       }
-      umma_commit_elect<false>(s_full);
-      return true;
     };
-    ApWork w = list.next(d, p.kv_heads, round);
-    if (w.n >= 0) ok = issue_s(w, 0, 0);
-    while (ok && w.n >= 0) {
-      const ApWork nx = list.next(d, p.kv_heads, round);
-      for (int j = 0; ok && j < w.n; ++j) {
-        ok = mbar_wait_warp(v_full, (t + j) & 1, status) && mbar_wait_warp(p_full, (t + j) & 1, status);
-        if (!ok) break;
+    ApCursor pc{{}, 0, 0}, sc{{}, 0, 0};
+    unit(sc, false);
+    unit(pc, true);
+    while (ok && pc.live()) {
+      // S(x) goes into the slot of P V(x - 2), issued before it: the tensor core takes them in
+      // order.  A unit's first S waits for Q, and lets the P V before it pass.
+      if (sc.live() && x <= i + 1 &&
+          (sc.j > 0 || x == i || __all_sync(0xffffffffu, mbar_done(q_full, units & 1)))) {
+        if ((sc.j == 0 && !mbar_wait_warp(q_full, units & 1, status)) ||
+            !mbar_wait_warp(&k_full[x & 1], (x >> 1) & 1, status)) { ok = false; break; }
+        if (sc.j == 0) ++units;
         tc_fence_after();
-        const int steps = j == w.n - 1 ? (w.tail + 15) / 16 : 8;
+        const uint32_t cols = sc.j == sc.w.n - 1 ? static_cast<uint32_t>(max(sc.w.tail, 1) + 15) / 16 * 16 : AP_KEYS;
+        const uint32_t idesc = idesc_m | ((cols >> 3) << 17);
+        const uint64_t ks = kd + static_cast<uint64_t>((x & 1) * AP_STEP >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)   // 16 keys per instruction
-          if (kk < steps)
-            umma_f16_ts_elect(tmem_base + 128, tmem_base + 64 + kk * 8, vd + static_cast<uint64_t>(kk * 2048 >> 4),
-                              idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-        if (j + 1 < w.n) {
-          ok = issue_s(w, j + 1, t + j + 1);
-        } else {
-          umma_commit_elect<false>(o_full);
-          if (nx.n >= 0) ok = issue_s(nx, 0, t + w.n);
+        for (int kk = 0; kk < 8; ++kk)
+          umma_f16_elect<false>(tmem_base + 64 * (x & 1),
+                                qd + (static_cast<uint64_t>((kk >> 2) * AP_HALF + (kk & 3) * 32) >> 4),
+                                ks + (static_cast<uint64_t>((kk >> 2) * AP_STEP_HALF + (kk & 3) * 32) >> 4), idesc,
+                                kk > 0);
+        umma_commit_elect<false>(&s_full[x & 1]);
+        if (++sc.j == sc.w.n) {
+          ++sc.k;
+          unit(sc, false);
         }
+        ++x;
+        continue;
       }
-      t += w.n;
-      w = nx;
+      if (!mbar_wait_warp(&v_full[i & 1], (i >> 1) & 1, status) ||
+          !mbar_wait_warp(&p_full[i & 1], (i >> 1) & 1, status)) { ok = false; break; }
+      tc_fence_after();
+      const int steps = pc.j == pc.w.n - 1 ? (pc.w.tail + 15) / 16 : AP_KEYS / 16;
+      const uint64_t vs = vd + static_cast<uint64_t>((i & 1) * AP_STEP >> 4);
+#pragma unroll
+      for (int kk = 0; kk < AP_KEYS / 16; ++kk)   // 16 keys per instruction
+        if (kk < steps)
+          umma_f16_ts_elect(tmem_base + 128, tmem_base + 64 * (i & 1) + kk * 8, vs + static_cast<uint64_t>(kk * 2048 >> 4),
+                            idesc_pv, (pc.j > 0 || kk > 0) ? 1u : 0u);
+      umma_commit_elect<false>(&pv_full[i & 1]);
+      if (++pc.j == pc.w.n) {
+        ++pc.k;
+        unit(pc, true);
+      }
+      ++i;
     }
     if (!ok) {   // no MMA may still run when TMEM is released
       umma_commit_elect<false>(drain);
@@ -413,67 +529,54 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     // ------------------------------------------------------------ softmax + epilogue
     const int row = warp * 32 + lane;
     const uint32_t lane_bits = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t tS = tmem_base + lane_bits, tO = tmem_base + lane_bits + 128;
+    const uint32_t tO = tmem_base + lane_bits + 128;
     const int row_pos = row / G, row_head = row - row_pos * G;
     const float sl2 = p.sm_scale * 1.4426950408889634f;
     bool ok = true;
-    int t = 0, units = 0;   // tiles of the units before this one, units with key tiles
-    for (int round = 0; ok; ++round) {
-      const ApWork w = list.get(d, p.kv_heads, round);
+    int t = 0;   // steps of the units before this one
+    for (int k = 0; ok; ++k) {
+      ApWork w;
+      if (!ap_read(ring, k, &w, status)) break;
+      warp_arrive(&ring->empty[k % AP_RING], lane);
       if (w.n < 0) break;
       const PackedSeq& sq = d.seq[w.u.s];
       const int pos = w.u.ct * P + row_pos;           // query position of this row
       const bool live = row < P * G && pos < sq.ql;
       const int lim = live ? max(0, sq.kl - sq.ql + 1 + pos) : 0;   // keys this row sees
-      // keys that every live row of this warp sees: tiles below need no mask
+      // keys that every live row of this warp sees: steps below need no mask
       const int lim_min = __reduce_min_sync(0xffffffffu, live ? lim : 0x7fffffff);
       const bool warp_live = __any_sync(0xffffffffu, live);
       float m_ref = -INFINITY;   // reference maximum, base-2 scaled; -inf: no score yet
       float l = 0.f;
       for (int j = 0; j < w.n; ++j) {
-        if (!mbar_wait_warp(s_full, (t + j) & 1, status)) { ok = false; break; }
+        const int g = t + j, slot = g & 1;
+        if (!mbar_wait_warp(&s_full[slot], (g >> 1) & 1, status)) { ok = false; break; }
         tc_fence_after();
-        const int k0 = (w.lo + j) * AP_ROWS;
-        const int ncols = j == w.n - 1 ? w.tail : AP_ROWS;   // the same for every row
+        const uint32_t tS = tmem_base + lane_bits + 64 * slot;
+        const int k0 = (w.lo + j) * AP_KEYS;
+        const int ncols = j == w.n - 1 ? w.tail : AP_KEYS;   // the same for every row
         if (warp_live) {   // (otherwise: no query in these 32 rows, and whatever O gets is dropped)
-          // The row's maximum over columns 0-63, then 64-127; the exponentials over 64-127, which are
-          // still in registers, then over 0-63, read again: 64 scores are held at a time.  (A whole
-          // row does not fit beside the rest, and what spills goes to L2: shared memory leaves little
-          // L1.)  P goes over columns 64-127 of S.  Columns past the cut are masked.
+          // columns past the cut are masked
           uint32_t r[2][32];
-          auto start = [&](int h) {
-            tmem_ld32_start(tS + 64 * h, r[0]);
-            tmem_ld32_start(tS + 64 * h + 32, r[1]);
-          };
-          auto finish = [&](int h) {
-            tmem_ld32_ready<true>(r[0]);
-            tmem_ld32_ready<false>(r[1]);
-            if (k0 + 64 * h + 64 > lim_min) {
+          tmem_ld32_start(tS, r[0]);
+          tmem_ld32_start(tS + 32, r[1]);
+          tmem_ld32_ready<true>(r[0]);
+          tmem_ld32_ready<false>(r[1]);
+          if (k0 + AP_KEYS > lim_min) {
 #pragma unroll
-              for (int i = 0; i < 64; ++i)
-                if (k0 + 64 * h + i >= lim) r[i >> 5][i & 31] = __float_as_uint(-INFINITY);
-            }
-          };
-          auto maximum = [&]() {
-            float m8[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) m8[k] = fmaxf(__uint_as_float(r[0][2 * k]), __uint_as_float(r[0][2 * k + 1]));
-#pragma unroll
-            for (int i = 16; i < 64; i += 16)
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                m8[k] = fmax3(m8[k], __uint_as_float(r[i >> 5][(i & 31) + 2 * k]),
-                              __uint_as_float(r[i >> 5][(i & 31) + 2 * k + 1]));
-            return fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-          };
-          start(0);
-          finish(0);
-          float mx2 = maximum();
-          if (ncols > 64) {
-            start(1);
-            finish(1);
-            mx2 = fmaxf(mx2, maximum());
+            for (int i = 0; i < 64; ++i)
+              if (k0 + i >= lim) r[i >> 5][i & 31] = __float_as_uint(-INFINITY);
           }
+          float m8[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) m8[k] = fmaxf(__uint_as_float(r[0][2 * k]), __uint_as_float(r[0][2 * k + 1]));
+#pragma unroll
+          for (int i = 16; i < 64; i += 16)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              m8[k] = fmax3(m8[k], __uint_as_float(r[i >> 5][(i & 31) + 2 * k]),
+                            __uint_as_float(r[i >> 5][(i & 31) + 2 * k + 1]));
+          float mx2 = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
           mx2 *= sl2;
           // the reference moves only when the maximum exceeds it by more than 8 (P <= 256)
           const float old = m_ref;
@@ -482,8 +585,11 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
           if (__any_sync(0xffffffffu, grow)) {
             const float f = grow ? exp2f(old - m_ref) : 1.0f;
             l *= f;
+            // (a row that has a score to rescale: a step of this unit came before)
+            if (!mbar_wait_warp(&pv_full[(g - 1) & 1], ((g - 1) >> 1) & 1, status)) { ok = false; break; }
+            tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {   // (P V of the tile before is complete: S came after it)
+            for (int c = 0; c < 8; ++c) {
               uint32_t o[16];
               tmem_ld16(tO + c * 16, o);
 #pragma unroll
@@ -496,34 +602,26 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
           const uint64_t sl2x2 = f2_pack(sl2, sl2);
           const uint64_t negm2 = f2_pack(neg, neg);
           uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
-          auto weights = [&](int h) {
 #pragma unroll
-            for (int c = 1; c >= 0; --c) {
-              if (64 * h + 32 * c >= ncols) continue;   // P V does not read further
+          for (int c = 0; c < 2; ++c) {
+            if (32 * c >= ncols) continue;   // P V does not read further
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                uint32_t pk[8];
+            for (int q = 0; q < 2; ++q) {
+              uint32_t pk[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float s0 = __uint_as_float(r[c][16 * q + 2 * i]), s1 = __uint_as_float(r[c][16 * q + 2 * i + 1]);
-                  const uint64_t x2 = f2_fma(f2_pack(s0, s1), sl2x2, negm2);
-                  float x0, x1;
-                  f2_unpack(x2, x0, x1);
-                  const float e0 = ex2_approx(x0);
-                  const float e1 = ex2_approx(x1);
-                  acc2[i & 3] = f2_add(acc2[i & 3], f2_pack(e0, e1));
-                  pk[i] = pack_bf16x2(e0, e1);
-                }
-                tmem_st8(tS + 64 + h * 32 + c * 16 + q * 8, pk);
+              for (int i = 0; i < 8; ++i) {
+                const float s0 = __uint_as_float(r[c][16 * q + 2 * i]), s1 = __uint_as_float(r[c][16 * q + 2 * i + 1]);
+                const uint64_t x2 = f2_fma(f2_pack(s0, s1), sl2x2, negm2);
+                float x0, x1;
+                f2_unpack(x2, x0, x1);
+                const float e0 = ex2_approx(x0);
+                const float e1 = ex2_approx(x1);
+                acc2[i & 3] = f2_add(acc2[i & 3], f2_pack(e0, e1));
+                pk[i] = pack_bf16x2(e0, e1);
               }
+              tmem_st8(tS + c * 16 + q * 8, pk);
             }
-          };
-          if (ncols > 64) {
-            weights(1);
-            start(0);
-            finish(0);
           }
-          weights(0);
           float a0, a1, b0, b1;
           f2_unpack(f2_add(acc2[0], acc2[1]), a0, a1);
           f2_unpack(f2_add(acc2[2], acc2[3]), b0, b1);
@@ -532,20 +630,21 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         }
         if (ncols & 15) {
           // clear V from the last visible key to the end of its 16-key step (the swizzle permutes
-          // inside a 128-byte row); S of this tile being complete, the V tile before has been used
-          if (!mbar_wait_warp(v_full, (t + j) & 1, status)) { ok = false; break; }
+          // inside a 128-byte row)
+          if (!mbar_wait_warp(&v_full[slot], (g >> 1) & 1, status)) { ok = false; break; }
           const int n_clear = ((ncols + 15) & ~15) - ncols;
           for (int i = row; i < n_clear * 16; i += 128)
-            *reinterpret_cast<uint4*>(sV + ((i >> 3) & 1) * AP_HALF + (ncols + (i >> 4)) * 128 + (i & 7) * 16) =
+            *reinterpret_cast<uint4*>(sV + slot * AP_STEP + ((i >> 3) & 1) * AP_STEP_HALF + (ncols + (i >> 4)) * 128 +
+                                      (i & 7) * 16) =
                 make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
         }
         tc_fence_before();
-        warp_arrive(p_full, lane);
+        warp_arrive(&p_full[slot], lane);
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (w.n > 0 && !mbar_wait_warp(o_full, units & 1, status)) { ok = false; break; }
+      if (!mbar_wait_warp(&pv_full[(t + w.n - 1) & 1], ((t + w.n - 1) >> 1) & 1, status)) { ok = false; break; }
       tc_fence_after();
       // where this row goes: fp32 partial of the key range, or the output.  32 whole rows leave
       // through TMA, 32 columns at a time (a warp's own stores, 32 rows of 16 bytes each, keep the
@@ -558,12 +657,12 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
                                         d.slot_rows + row
                               : static_cast<size_t>(sq.q0 + pos) * p.ldo + (w.u.h * G + row_head) * 128;
       if (split && live) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m_ref, l);
-      if (warp_live && (w.n > 0 || !split)) {   // (a range without a key has weight 0, whatever its O)
+      if (warp_live) {   // (a range without a key has weight 0, whatever its O)
         const bool whole = !split && p.tma_out && __all_sync(0xffffffffu, live);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t r[32];
-          if (w.n > 0) tmem_ld32(tO + 32 * c, r);
+          tmem_ld32(tO + 32 * c, r);
           if (split) {
             if (!live) continue;
             float4* dst = reinterpret_cast<float4*>(p.part_o + at * 128 + c * 32);
@@ -603,7 +702,6 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         }
       }
       t += w.n;
-      if (w.n > 0) ++units;
       tc_fence_before();   // O has been read before the next unit's P lets P V write it
     }
   }
@@ -1006,12 +1104,12 @@ __global__ void __launch_bounds__(32 * AP_JOIN_WARPS) ap_join_kernel(const __gri
 //    costs less than a second kernel (about 12 us).
 //  * tile kernel: key ranges are split when the longest unit would outlast the
 //    average load of an SM, into ranges of about that average, at least
-//    AP_MIN_RANGE key tiles (a range costs a partial result and the joining
+//    AP_MIN_RANGE steps of keys (a range costs a partial result and the joining
 //    kernel).
 //  * token kernel: two CTAs fit on an SM; ranges are as long as gives every
 //    place one CTA, but between AT_MIN_KEYS (fewer keys do not pay for a
 //    partial result) and AT_MAX_KEYS (shorter CTAs even out ragged lengths).
-constexpr int AP_MIN_RANGE = 4;
+constexpr int AP_MIN_RANGE = 8;
 constexpr int AT_MIN_KEYS = 256, AT_MAX_KEYS = 512, AT_JOIN_KEYS = 2048;
 
 struct PlanSeq {
@@ -1074,32 +1172,32 @@ void packed_plan(const int32_t* spans, int n, int heads, int kv_heads, int num_s
   if (big.empty()) return;
   PackedPlan* d = tile;
   auto tiles = [&](const PlanSeq& s) { return (s.ql + d->P - 1) / d->P; };
-  auto key_tiles = [&](const PlanSeq& s, int ct) {   // of query tile ct
+  auto steps = [&](const PlanSeq& s, int ct) {   // of query tile ct over its keys
     const long long end = static_cast<long long>(s.kl) - s.ql + std::min((ct + 1) * d->P, s.ql);
-    return end > 0 ? (end + AP_ROWS - 1) / AP_ROWS : 0ll;
+    return end > 0 ? (end + AP_KEYS - 1) / AP_KEYS : 0ll;
   };
   long long total = 0, longest = 0;
   for (const PlanSeq& s : big) {
     const int t = tiles(s);
-    for (int c = 0; c < t; ++c) total += key_tiles(s, c) * kv_heads;
-    longest = std::max(longest, key_tiles(s, t - 1));
+    for (int c = 0; c < t; ++c) total += steps(s, c) * kv_heads;
+    longest = std::max(longest, steps(s, t - 1));
   }
   const long long share = (total + num_sms - 1) / num_sms;
   const long long range = std::max<long long>(AP_MIN_RANGE, share);
   if (longest >= 2 * range)
     for (PlanSeq& s : big) {
-      const long long k = key_tiles(s, tiles(s) - 1);
+      const long long k = steps(s, tiles(s) - 1);
       if (k >= 2 * range) s.nsp = static_cast<int>((k + range - 1) / range);
     }
   plan_finish(big, kv_heads, d);
   // Exact order, longest unit first, where the table holds it and no unit is split (a counting
-  // sort over the key tiles of a unit).
+  // sort over the steps of a unit).
   if (d->slots > 0 || d->units > AP_MAX_ORDER * kv_heads || longest > AP_MAX_ORDER) return;
   std::vector<int> at(static_cast<size_t>(longest) + 2, 0);
   for (int pass = 0; pass < 2; ++pass) {
     for (int i = 0; i < d->n_seqs; ++i)
       for (int c = tiles(big[i]) - 1; c >= 0; --c) {
-        const size_t cost = static_cast<size_t>(longest - key_tiles(big[i], c));   // 0: the longest
+        const size_t cost = static_cast<size_t>(longest - steps(big[i], c));   // 0: the longest
         if (pass == 0) ++at[cost + 1];
         else d->order[at[cost]++] = static_cast<uint32_t>(i) << 24 | static_cast<uint32_t>(c);
       }
@@ -1180,7 +1278,7 @@ static int launch_tile(const PackedAttnParams& a, const PackedPlan& d, uint8_t* 
   ap_params(a, d, scratch, &p);
   CUtensorMap tq, tk, tv, to;
   if (!make_tmap_rows3(&tq, a.q, 128, a.heads, a.q_rows, static_cast<uint64_t>(a.ldq) * 2, 64, d.G, d.P) ||
-      !ap_kv_maps(a, &tk, &tv, AP_ROWS))
+      !ap_kv_maps(a, &tk, &tv, AP_KEYS))
     return -2;
   // output boxes: the 32 rows of a softmax warp, min(G, 32) heads x 32 / G positions
   p.tma_out = 32 % d.G == 0 || d.G % 32 == 0;
@@ -1189,7 +1287,7 @@ static int launch_tile(const PackedAttnParams& a, const PackedPlan& d, uint8_t* 
   else if (!make_tmap_rows3(&to, a.o, 128, a.heads, a.q_rows, static_cast<uint64_t>(a.ldo) * 2, 32, box_heads,
                             32 / box_heads))
     return -2;
-  launch_pdl(ap_kernel<Plan>, dim3(std::min(d.units, 2 * a.num_sms)), dim3(AP_THREADS), AP_SMEM, st, 1, tq, tk, tv, to,
+  launch_pdl(ap_kernel<Plan>, dim3(d.units), dim3(AP_THREADS), AP_SMEM, st, 1, tq, tk, tv, to,
              p);
   return launch_result() || launch_join(p, st) ? -1 : 0;
 }
