@@ -54,6 +54,7 @@ struct MmParams {
   int num_kb[MM_MAX_PROB];     // 64-element K blocks of one segment
   int tiles_end[MM_MAX_PROB];  // running number of tiles
   int group_m[MM_MAX_PROB];    // tile order (tile_coords)
+  int bn;                      // persistent kernel, K-major B: columns of a pair's tile (256, 192 or 128)
   int segs;                    // 2: operands a[0], b[0], then a[1], b[1], into one sum
   uint16_t* y[MM_MAX_PROB];    // MM_DGATE: dg, du and, unless null, h, each [M, F]
   int ldy[MM_MAX_PROB];
@@ -67,7 +68,7 @@ struct MmParams {
 };
 
 constexpr int MM_TILE = 128 * 128;   // bytes of a stage's A or B tile of one CTA: 128 x 64 bf16
-constexpr int MM_BN = 256;           // persistent kernel: columns of a pair's tile
+constexpr int MM_BN = 256;           // most columns of a pair's tile
 constexpr int MM_STAGES = 6;
 constexpr int MM_OUT = 32 * 64;      // bytes of an epilogue chunk of 32 rows x 32 bf16 columns
 // Persistent kernel: stages of the operands, and chunks of shared memory per
@@ -292,17 +293,17 @@ __device__ __forceinline__ void mm_fetch(const MmMaps& maps, MmStage& s, int row
 // warp's last TMEM read.  A thread holds one row, so its own accesses would be
 // 16 bytes in each of 32 rows, 32 passes of the load/store unit each; instead a
 // warp's 32 x 32 chunk goes through shared memory and TMA brings the inputs and
-// takes the outputs (TMA keeps to the rows and columns that exist).  Rows that
-// are not 16-byte aligned (p.vec == 0) are accessed directly.
+// takes the outputs (TMA keeps to the rows and columns that exist).  TMA needs
+// rows that are 16-byte aligned; others (p.vec == 0) are read and written by
+// the warp, one value per lane and 32 of a row at a time.
 // Swizzles: 16-byte group q of row r of a bf16 chunk lies at q ^ (r / 2 mod 4),
 // of an fp32 chunk at q ^ (r mod 8).
 template <int EPI>
 __device__ __forceinline__ bool mm_epilogue(const MmMaps& maps, const MmParams& p, int pr, uint64_t* tfull,
                                             uint32_t tfull_phase, uint32_t tacc, int m0, int n0, int quarter,
-                                            int half, int lane, uint32_t tempty_addr, MmStage& s) {
-  constexpr int W = EPI == MM_GATE ? MM_BN / 2 : MM_BN;   // output columns of a tile
-  constexpr int CH = W / 32;
-  const int row0 = m0 + quarter * 32, m = row0 + lane, N = p.N[pr];
+                                            int half, int lane, uint32_t tempty_addr, MmStage& s, int W) {
+  const int CH = W / 32;   // (W: output columns of a tile)
+  const int row0 = m0 + quarter * 32, N = p.N[pr];
   const bool vec = EPI != MM_LINEAR || p.vec;
   const bool rows_in = row0 < p.M[pr];
   const bool has_in = EPI == MM_DGATE || (EPI == MM_LINEAR && p.res && vec);
@@ -340,15 +341,6 @@ __device__ __forceinline__ bool mm_epilogue(const MmMaps& maps, const MmParams& 
         u[i] = EPI == MM_GATE ? __uint_as_float(r2[8 * q + i]) : 0.f;
       }
     };
-    if (!vec) {
-      if (m < p.M[pr])
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          sums(q);
-          mm_out8<EPI>(p, pr, m, col0 + q * 8, v, u);
-        }
-      continue;
-    }
     if (has_in) {
       if (!mbar_wait_warp(s.bar, s.phase, p.status)) return false;
       s.phase ^= 1u;
@@ -380,9 +372,24 @@ __device__ __forceinline__ bool mm_epilogue(const MmMaps& maps, const MmParams& 
     float xg[8] = {}, xu[8] = {};
     if constexpr (EPI == MM_LINEAR) {
       uint8_t* at = s.at(s.turn & 1);
+      const int rows = min(32, p.M[pr] - row0);
+      const bool col_in = col0 + lane < N;
+      auto value = [&](int i) {   // of row i, this lane's column
+        return reinterpret_cast<uint16_t*>(at + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4)) + (lane & 7);
+      };
+      if (!vec && p.res) {
+        const uint16_t* src = p.res + static_cast<size_t>(row0) * p.ld_res + col0 + lane;
+        uint16_t x16[32];   // (all asked for before the first is used)
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          x16[i] = col_in && i < rows ? src[static_cast<size_t>(i) * p.ld_res] : static_cast<uint16_t>(0);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) *value(i) = x16[i];
+        __syncwarp();
+      }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (has_in) {
+        if (p.res) {
           const uint4 w = *group(at, q);
           x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
         }
@@ -390,7 +397,16 @@ __device__ __forceinline__ bool mm_epilogue(const MmMaps& maps, const MmParams& 
         mm_math8<EPI>(p, v, u, col0 + q * 8, N - col0 - q * 8, x, xg, xu, o0, o1, o2);
         put(at, q, o0);
       }
-      send(&maps.y[pr], at, col0, 0);
+      if (vec) {
+        send(&maps.y[pr], at, col0, 0);
+      } else {
+        __syncwarp();
+        uint16_t* dst = p.y[pr] + static_cast<size_t>(row0) * p.ldy[pr] + col0 + lane;
+        if (col_in)
+#pragma unroll 8
+          for (int i = 0; i < rows; ++i) dst[static_cast<size_t>(i) * p.ldy[pr]] = *value(i);
+        __syncwarp();
+      }
       ++s.turn;
     } else if constexpr (EPI == MM_GATE) {
       uint8_t* at = s.at(p.gu ? 0 : s.turn & 1);
@@ -447,8 +463,8 @@ __device__ __forceinline__ bool mm_epilogue(const MmMaps& maps, const MmParams& 
 }
 
 // Product and tile coordinates of a tile number, for tiles of BM rows and W columns.
-template <int BM, int W>
-__device__ __forceinline__ void mm_tile(const MmParams& p, int tile, int& pr, int& mt, int& nt) {
+template <int BM>
+__device__ __forceinline__ void mm_tile(const MmParams& p, int tile, int W, int& pr, int& mt, int& nt) {
   pr = 0;
   while (pr < p.n_prob - 1 && tile >= p.tiles_end[pr]) ++pr;
   if (pr > 0) tile -= p.tiles_end[pr - 1];
@@ -483,22 +499,24 @@ __device__ __forceinline__ uint64_t mm_desc(const uint8_t* tile) {
   return MN ? umma_desc_mnmajor_sw128(smem_u32(tile), 8192) : umma_desc_kmajor_sw128(smem_u32(tile));
 }
 
-template <bool PAIR, bool AMN, bool BMN>
-constexpr uint32_t mm_idesc() {
-  return umma_idesc(false, PAIR ? 256 : 128, PAIR ? MM_BN : 128) | (AMN ? (1u << 15) : 0u) | (BMN ? (1u << 16) : 0u);
+template <bool AMN, bool BMN>
+__device__ __forceinline__ uint32_t mm_idesc(int n) {   // of a pair: 256 x n
+  return umma_idesc(false, 256, n) | (AMN ? (1u << 15) : 0u) | (BMN ? (1u << 16) : 0u);
 }
 
 // ---------------------------------------------------------------- large products
 //
 // A pair of CTAs (one per SM) shares a 256 x 256 tile (cta_group::2): each
 // loads 128 rows of A and 128 rows of B, and the even CTA issues the MMAs for
-// both.  Persistent over tiles; the accumulator is double-buffered in TMEM, so
+// both.  Where they fill the last round better, tiles are 192 or 128 columns
+// wide.  Persistent over tiles; the accumulator is double-buffered in TMEM, so
 // the epilogue of a tile overlaps the MMAs of the next.
 template <bool AMN, bool BMN, int EPI>
 __global__ void __launch_bounds__(MM_THREADS, 1)
     mm_kernel(const __grid_constant__ MmMaps maps, const __grid_constant__ MmParams p) {
   constexpr int STAGES = MmCfg<EPI>::STAGES;
-  constexpr int W = EPI == MM_GATE ? MM_BN / 2 : MM_BN;
+  const int bn = BMN ? MM_BN : p.bn;   // columns of the accumulator
+  const int W = EPI == MM_GATE ? bn / 2 : bn;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -555,9 +573,9 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     bool ok = true;
     for (int tile = worker; tile < num_tiles && ok; tile += workers) {
       int pr, mt, nt;
-      mm_tile<256, W>(p, tile, pr, mt, nt);
+      mm_tile<256>(p, tile, W, pr, mt, nt);
       const int m0 = mt * 256 + rank * 128;
-      const int n0 = EPI == MM_GATE ? nt * W : nt * MM_BN + rank * 128;
+      const int n0 = EPI == MM_GATE ? nt * W : nt * bn + rank * (bn / 2);
       const int num_kb = p.num_kb[pr];
       for (int seg = 0; seg < p.segs && ok; ++seg) {   // segs == 2 only for a single product
         const CUtensorMap* ma = &maps.a[pr + seg];
@@ -565,7 +583,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!mbar_wait_warp(&empty[stage], phase ^ 1u, p.status)) { ok = false; break; }
           const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
-          if (rank == 0) mbar_expect_elect(&full[stage], 4 * MM_TILE);
+          if (rank == 0) mbar_expect_elect(&full[stage], static_cast<uint32_t>(2 * MM_TILE + bn * 128));
           mm_load<true, AMN>(ma, fb, sA + stage * MM_TILE, kb * 64, m0);
           mm_load<true, BMN>(mb, fb, sB + stage * MM_TILE, kb * 64, n0);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -595,7 +613,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     // are uniform over a converged warp reach the tensor core's instruction
     // without a move per lane (an MMA issued under a lane test took 54 clocks).
     if (rank == 0) {
-      constexpr uint32_t idesc = mm_idesc<true, AMN, BMN>();
+      const uint32_t idesc = mm_idesc<AMN, BMN>(bn);
       const uint64_t adesc = mm_desc<AMN>(sA), bdesc = mm_desc<BMN>(sB);
       int stage = 0;
       uint32_t phase = 0;
@@ -604,7 +622,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
       bool ok = true;
       for (int tile = worker; tile < num_tiles && ok; tile += workers) {
         int pr, mt, nt;
-        mm_tile<256, W>(p, tile, pr, mt, nt);
+        mm_tile<256>(p, tile, W, pr, mt, nt);
         const int total_kb = p.num_kb[pr] * p.segs;
         if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, p.status))) { ok = false; break; }
         tc_fence_after();
@@ -639,10 +657,10 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     MmStage stage{sOut + (warp - 2) * MmCfg<EPI>::CHUNKS * MM_OUT, &xfull[warp - 2], 0, 0};
     for (int tile = worker; tile < num_tiles; tile += workers) {
       int pr, mt, nt;
-      mm_tile<256, W>(p, tile, pr, mt, nt);
+      mm_tile<256>(p, tile, W, pr, mt, nt);
       if (!mm_epilogue<EPI>(maps, p, pr, &tfull[acc], acc_phase, tmem_base + static_cast<uint32_t>(acc * MM_BN),
                             mt * 256 + rank * 128, nt * W, quarter, half, lane,
-                            mapa_shared(smem_u32(&tempty[acc]), 0), stage))
+                            mapa_shared(smem_u32(&tempty[acc]), 0), stage, W))
         break;
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
@@ -719,7 +737,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     tmem_relinquish_pair();
   }
   int pr, mt, nt;
-  mm_tile<256, W>(p, static_cast<int>(blockIdx.x) / (2 * S), pr, mt, nt);
+  mm_tile<256>(p, static_cast<int>(blockIdx.x) / (2 * S), W, pr, mt, nt);
   const int total_kb = p.num_kb[pr] * p.segs;
   const int lo = total_kb * part / S, hi = total_kb * (part + 1) / S;
   const int m0 = mt * 256 + rank * 128;
@@ -763,7 +781,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
     if (rank == 0) {
-      constexpr uint32_t idesc = mm_idesc<true, AMN, BMN>();
+      const uint32_t idesc = mm_idesc<AMN, BMN>(MM_BN);
       const uint64_t adesc = mm_desc<AMN>(sA), bdesc = mm_desc<BMN>(sB);
       const uint16_t both = static_cast<uint16_t>(0x3u << even);
       int stage = 0;
@@ -1246,11 +1264,13 @@ static int cluster_places(K kern, int ctas, int smem, int num_sms) {
 }
 
 // Kernel of a launch, by estimates in clocks.
-// 256 x 256 tiles: rounds of tiles times K blocks times 600 (32 KB into each
-// SM), plus what starts and ends a tile (the launch, the first loads, the sums'
-// way out): 14000, which the persistent kernel pays once, or per round 15000
-// with shared K, 23000 with the five accesses of MM_DGATE.  Measured, whole K /
-// parts of K: 512 x 4096 x 11008 55 / 38 us.
+// Tiles of 256 rows: rounds of tiles times K blocks times 600 (256 columns: 32
+// KB into each SM), 510 (192) or 440 (128), plus what starts and ends a tile (the
+// launch, the first loads, the sums' way out): 14000, which the persistent kernel
+// pays once, or per round 15000 with shared K, 23000 with the five accesses of
+// MM_DGATE, 25000 where y takes single values.  Measured, whole K / parts of K:
+// 512 x 4096 x 11008 55 / 38 us; tiles of 256 / 192 / 128 columns: 768 x 4096 x
+// 11008 74 / 56 / 89 us, 1000 x 4096 x 11008 70 / 100 / 88.
 // mm_rows_kernel: 8000 per round and 9 S T for the exchange, plus the largest of
 //   a CTA's K blocks, each its loads' latency (340, or 2000 over the stages) or
 //   its bytes at 84 per clock;
@@ -1260,6 +1280,7 @@ static int cluster_places(K kern, int ctas, int smem, int num_sms) {
 // x 22016 x 4096 51 / 39, 333 x 4096 x 4096 19.7 / 15.8; 256 x 6144 x 4096 19.9
 // / 20.5, 512 x 6144 x 4096 27.8 / 30.
 struct MmShape {
+  int bn;       // columns of the persistent kernel's tiles
   bool rows;    // mm_rows_kernel
   int S;        // parts of K (1 and not rows: the persistent kernel)
   int T, stages;
@@ -1273,15 +1294,21 @@ static bool mm_shape(MmParams p, int num_sms, MmShape* pick) {
   long kb = 0;
   for (int i = 0; i < p.n_prob; ++i) kb = kb > p.num_kb[i] * p.segs ? kb : p.num_kb[i] * p.segs;
   auto rounds = [](long n, long places) { return (n + places - 1) / places; };
+  long best = 0;
+  for (int bn = 256; bn >= (BMN ? 256 : 128); bn -= 64) {
+    const long cost = rounds(mm_count_tiles(p, 256, bn / W_DIV), num_sms / 2) * kb * (bn == 256 ? 600 : (bn == 192 ? 510 : 440)) + 14000;
+    if (best == 0 || cost < best) {
+      best = cost;
+      *pick = {bn, false, 1, 0, 0};
+    }
+  }
   const long tiles = mm_count_tiles(p, 256, 256 / W_DIV);
-  long best = rounds(tiles, num_sms / 2) * kb * 600 + 14000;
-  *pick = {false, 1, 0, 0};
   for (int s = 2; s <= 4; s *= 2) {
     const long cost = rounds(tiles, cluster_places(pair_kern, 2 * s, MS_SMEM, num_sms)) *
-                          (rounds(kb, s) * 600 + (EPI == MM_DGATE ? 23000 : 15000));
+                          (rounds(kb, s) * 600 + (EPI == MM_DGATE ? 23000 : (p.vec ? 15000 : 25000)));
     if (cost < best) {
       best = cost;
-      *pick = {false, s, 0, 0};
+      *pick = {256, false, s, 0, 0};
     }
   }
   if constexpr (!AMN) {
@@ -1302,7 +1329,7 @@ static bool mm_shape(MmParams p, int num_sms, MmShape* pick) {
                                                             std::max(n * kb * mr_stage(T) / 9000, nw * kb * MM_TILE / 3400));
         if (cost < best) {
           best = cost;
-          *pick = {true, s, T, stages};
+          *pick = {0, true, s, T, stages};
         }
       }
     }
@@ -1339,9 +1366,10 @@ static int mm_launch(const MmOperand* A, const MmOperand* B, int n_ops_a, int n_
   MmMaps maps;
   for (int i = 0; i < MM_MAX_PROB; ++i) {
     if (!mm_map(&maps.a[i], A[i < n_ops_a ? i : 0], AMN, 128)) return -2;
-    if (!mm_map(&maps.b[i], B[i < n_ops_b ? i : 0], BMN, 128)) return -2;
+    if (!mm_map(&maps.b[i], B[i < n_ops_b ? i : 0], BMN, shape.bn / 2)) return -2;
   }
-  const long tiles = mm_count_tiles(p, 256, MM_BN / W_DIV);
+  p.bn = shape.bn;
+  const long tiles = mm_count_tiles(p, 256, shape.bn / W_DIV);
   if (shape.S > 1) {
     launch_pdl(mm_split_kernel<AMN, BMN, EPI>, dim3(static_cast<unsigned>(tiles) * 2 * shape.S), dim3(MM_THREADS),
                MS_SMEM, st, static_cast<unsigned>(2 * shape.S), maps, p, shape.S);

@@ -358,8 +358,8 @@ def test_linear_few_rows(ctx, M, n, k):
     check_linear(ctx, a, w, None, qi.QI_ACT_NONE)
 
 
-@pytest.mark.parametrize("M", [1, 5, 40, 260])
-@pytest.mark.parametrize("n", [1, 3, 33, 255, 257])
+@pytest.mark.parametrize("M", [1, 5, 40, 260, 777])
+@pytest.mark.parametrize("n", [1, 3, 33, 255, 257, 1001])
 def test_linear_odd_outputs(ctx, M, n):
     """Any n and any row distance of y and residual: odd ones have unaligned rows."""
     k = 136
@@ -376,6 +376,13 @@ def test_linear_odd_outputs(ctx, M, n):
 def test_linear_full_width(ctx, M, n, k):
     check_linear(ctx, rand(M, k), rand(n, k, seed=1, scale=0.02), rand(n, seed=2, scale=0.02),
                  qi.QI_ACT_GELU_TANH, rand(M, n, seed=3))
+
+
+@pytest.mark.parametrize("M,n", [(600, 1100), (1300, 1100), (1000, 2300), (520, 4000), (1100, 130)])
+def test_linear_tile_widths(ctx, M, n):
+    """Sizes whose tiles are 256, 192 or 128 columns wide, with cut last tiles."""
+    a, w, b = rand(M, 520), rand(n, 520, seed=1, scale=0.05), rand(n, seed=2)
+    check_linear(ctx, a, w, b, qi.QI_ACT_SILU, rand(M, n, seed=3))
 
 
 @pytest.mark.parametrize("M", [1, 12, 70, 513])
@@ -466,7 +473,7 @@ def check_backward(ctx, w, x, wg, wu, wd, act, gu, dy):
 
 
 SHAPES = [(1, 64, 128), (16, 200, 72), (25, 136, 328), (32, 520, 200), (33, 64, 4096), (40, 4096, 64), (9, 64, 8192), (17, 256, 520), (100, 512, 1384), (333, 1024, 2816), (129, 8, 8),
-          (700, 1032, 264)]
+          (700, 1032, 264), (780, 264, 2000)]
 
 
 @pytest.mark.parametrize("act", [qi.QI_ACT_SILU, qi.QI_ACT_GELU_TANH])
