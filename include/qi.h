@@ -394,8 +394,10 @@ int qi_attn_split_plan(int Sk, int heads, const qi_groups* groups, int num_sms,
  * function below returns for the same table (0 for most: only sequences whose
  * keys are many and queries few are split over their keys), contents
  * irrelevant.  Scores, maxima, sums and O are fp32; the weights enter P V as bf16.
- * The result of a sequence depends on the table only through the split of its
- * key range (rounding). */
+ * The other sequences of a table never reach a sequence's result, but the table
+ * as a whole decides which kernel runs it and into how many ranges its keys are
+ * split, and with them the order of its sums: the same table gives the same bits
+ * every time, another table the same result within rounding. */
 #define QI_MAX_SEQS 256
 int qi_attn_causal_packed_workspace_bytes(qi_ctx* ctx, const int32_t* spans, int n_seqs, int heads,
                                           int kv_heads, size_t* bytes);
@@ -416,7 +418,9 @@ typedef enum {
  * fp32 until the one rounding at the end.  residual may be NULL, or y itself
  * (same pointer and ld: y is updated in place).  Any n >= 1 and any ldy,
  * ld_residual >= n (rows that are 16-byte aligned are written faster); k and
- * lda multiples of 8; a, W and bias 16-byte aligned. */
+ * lda multiples of 8; a, W and bias 16-byte aligned.  Which kernel runs, and
+ * with it the order of a sum, goes by M, k and n; the same call gives the same
+ * bits every time. */
 int qi_linear_act(qi_ctx* ctx, const uint16_t* a, int M, int lda, const qi_linear_bf16* w, int act,
                   const uint16_t* residual, int ld_residual, uint16_t* y, int ldy, void* stream);
 
