@@ -548,6 +548,19 @@ def _new(shape, like: torch.Tensor, stream, dtype=torch.bfloat16):
         return like.new_empty(shape, dtype=dtype)
 
 
+def _out(ctx: Context, t: Optional[torch.Tensor], name: str, rows: int, cols: int, like: torch.Tensor, stream):
+    """(tensor, pointer, leading dimension) of a bf16 output: the caller's, or a new one."""
+    if t is None:
+        if stream is None and like.shape == (rows, cols) and like.is_contiguous():
+            t = torch.empty_like(like)          # (the quickest way to one)
+        else:
+            t = _new((rows, cols), like, stream)
+        return t, t.data_ptr(), cols
+    if t.shape[0] != rows:
+        raise ValueError(f"{name} must have {rows} rows")
+    return (t, *_rows(ctx, t, name, cols))
+
+
 def _on(ctx: Context, stream) -> int:
     """Stream handle of a call: `stream`, or the current one of the context's device."""
     if stream is not None:
@@ -578,14 +591,13 @@ def qi_attn_causal_packed(ctx: Context, q, k, v, spans: torch.Tensor, heads: int
     new o outside every sequence are not written."""
     W, KW = heads * 128, kv_heads * 128
     st = _on(ctx, stream)
-    if o is None:
-        o = _new((q.shape[0], W), q, stream)
-    if k.shape[0] != v.shape[0] or o.shape[0] != q.shape[0]:
-        raise ValueError("k and v, and q and o, must have the same number of rows")
     qp, ldq = _rows(ctx, q, "q", W)
     kp, ldk = _rows(ctx, k, "k", KW)
     vp, ldv = _rows(ctx, v, "v", KW)
-    op, ldo = _rows(ctx, o, "o", W)
+    q_rows, k_rows = q.shape[0], k.shape[0]
+    if v.shape[0] != k_rows:
+        raise ValueError("k and v must have the same number of rows")
+    o, op, ldo = _out(ctx, o, "o", q_rows, W, q, stream)
     L, table, n_seqs = lib(), _spans(spans), spans.shape[0]
     if workspace is None:
         size = C.c_size_t()
@@ -594,7 +606,7 @@ def qi_attn_causal_packed(ctx: Context, q, k, v, spans: torch.Tensor, heads: int
         if n:
             workspace = _new(n, q, stream, torch.uint8)
     check(L.qi_attn_causal_packed(
-        ctx.handle, qp, ldq, q.shape[0], kp, ldk, vp, ldv, k.shape[0], heads, kv_heads, 128,
+        ctx.handle, qp, ldq, q_rows, kp, ldk, vp, ldv, k_rows, heads, kv_heads, 128,
         table, n_seqs, sm_scale if sm_scale is not None else 128 ** -0.5, op, ldo,
         *_scratch(workspace, q), st))
     return o
@@ -605,14 +617,12 @@ def qi_linear_act(ctx: Context, a: torch.Tensor, w: qi_linear_bf16, act: int = Q
                   stream=None):
     """y = act(a w^T + bias) + residual, bf16 (residual may be y)."""
     st = _on(ctx, stream)
-    M = a.shape[0]
-    if y is None:
-        y = _new((M, w.n), a, stream)
-    if y.shape[0] != M or (residual is not None and residual.shape[0] != M):
-        raise ValueError("a, residual and y must have the same number of rows")
     ap, lda = _rows(ctx, a, "a", w.k)
-    rp, ldr = _rows(ctx, residual, "residual", w.n)
-    yp, ldy = _rows(ctx, y, "y", w.n)
+    M, n = a.shape[0], w.n
+    if residual is not None and residual.shape[0] != M:
+        raise ValueError("a and residual must have the same number of rows")
+    rp, ldr = _rows(ctx, residual, "residual", n)
+    y, yp, ldy = _out(ctx, y, "y", M, n, a if residual is None else residual, stream)
     check(lib().qi_linear_act(ctx.handle, ap, M, lda, C.byref(w), act, rp, ldr, yp, ldy, st))
     return y
 
@@ -644,19 +654,17 @@ def qi_gated_ffn_forward(ctx: Context, w: qi_gated_ffn, x: torch.Tensor,
     """y = (act(x gate^T) * (x up^T)) down^T + residual.  save=True (or a gate_up
     buffer [M, 2 mlp] fp32) also returns what the backward call needs: (y, gate_up)."""
     st = _on(ctx, stream)
-    M = x.shape[0]
-    if y is None:
-        y = _new((M, w.hidden), x, stream)
-    if y.shape[0] != M or (residual is not None and residual.shape[0] != M):
-        raise ValueError("x, residual and y must have the same number of rows")
+    M, H = x.shape[0], w.hidden
+    xp, ldx = _rows(ctx, x, "x", H)
+    if residual is not None and residual.shape[0] != M:
+        raise ValueError("x and residual must have the same number of rows")
+    rp, ldr = _rows(ctx, residual, "residual", H)
+    y, yp, ldy = _out(ctx, y, "y", M, H, x, stream)
     if save and gate_up is None:
         gate_up = _new((M, 2 * w.mlp), x, stream, torch.float32)
     _whole(gate_up, "gate_up", (M, 2 * w.mlp), x, torch.float32)
     if workspace is None:
         workspace = _new(qi_gated_ffn_workspace_bytes(w, M), x, stream, torch.uint8)
-    xp, ldx = _rows(ctx, x, "x", w.hidden)
-    rp, ldr = _rows(ctx, residual, "residual", w.hidden)
-    yp, ldy = _rows(ctx, y, "y", w.hidden)
     check(lib().qi_gated_ffn_forward(ctx.handle, C.byref(w), xp, M, ldx, rp, ldr, yp, ldy,
                                      ptr(gate_up), *_scratch(workspace, x), st))
     return (y, gate_up) if gate_up is not None else y
@@ -674,6 +682,8 @@ def qi_gated_ffn_backward(ctx: Context, w: qi_gated_ffn, x: torch.Tensor, dy: to
     if dy.shape[0] != M:
         raise ValueError("x and dy must have the same number of rows")
     _whole(gate_up, "gate_up", (M, 2 * F), x, torch.float32)
+    if not set(want) <= {"dx", "dgate", "dup", "ddown"}:
+        raise ValueError(f"want names dx, dgate, dup, ddown, not {want}")
     out = {}
     for name, t, shape in (("dx", dx, (M, H)), ("dgate", dgate, (F, H)), ("dup", dup, (F, H)),
                            ("ddown", ddown, (H, F))):
