@@ -1230,13 +1230,15 @@ static long mm_count_tiles(MmParams& p, int bm, int w) {
   return tiles;
 }
 
-// Clusters of `ctas` CTAs of a kernel that run at the same time on the current
-// device (the SMs of one GPC hold a whole number of clusters: 74, 33 and 15
-// clusters of 2, 4 and 8 on 148 SMs), asked once per device.
+// Clusters of `ctas` CTAs, one CTA per SM, that run at the same time on the
+// current device (the SMs of one GPC hold a whole number of clusters: 74, 33 and
+// 15 clusters of 2, 4 and 8 on 148 SMs).  Asked once per device, and for every
+// kernel with the same shared memory, so that the answer, and with it the order
+// of a product's sums, does not depend on which call came first.
 template <class K>
-static int cluster_places(K kern, int ctas, int smem, int num_sms) {
+static int cluster_places(K kern, int ctas, int num_sms) {
   if (ctas <= 1) return num_sms;
-  static std::atomic<int> known[64][4];   // per kernel instantiation; 0: not asked yet
+  static std::atomic<int> known[64][4];   // 0: not asked yet
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return num_sms / ctas;
   const int slot = ctas == 2 ? 0 : (ctas == 4 ? 1 : 2);
@@ -1251,7 +1253,7 @@ static int cluster_places(K kern, int ctas, int smem, int num_sms) {
     attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
     cfg.blockDim = dim3(MM_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.dynamicSmemBytes = MS_SMEM;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
@@ -1304,7 +1306,7 @@ static bool mm_shape(MmParams p, int num_sms, MmShape* pick) {
   }
   const long tiles = mm_count_tiles(p, 256, 256 / W_DIV);
   for (int s = 2; s <= 4; s *= 2) {
-    const long cost = rounds(tiles, cluster_places(pair_kern, 2 * s, MS_SMEM, num_sms)) *
+    const long cost = rounds(tiles, cluster_places(pair_kern, 2 * s, num_sms)) *
                           (rounds(kb, s) * 600 + (EPI == MM_DGATE ? 23000 : (p.vec ? 15000 : 25000)));
     if (cost < best) {
       best = cost;
@@ -1323,7 +1325,7 @@ static bool mm_shape(MmParams p, int num_sms, MmShape* pick) {
         // two CTAs per SM when there are more CTAs than SMs and TMEM and shared memory allow it
         const int per_sm = T <= 128 && n * s > num_sms ? 2 : 1;
         const int stages = std::min(MR_MAX_STAGES, ((per_sm == 2 ? 115712 : 232448) - 1280) / mr_stage(T));
-        const long r = rounds(n, static_cast<long>(per_sm) * cluster_places(kern, s, mr_smem(T, stages), num_sms));
+        const long r = rounds(n, static_cast<long>(per_sm) * cluster_places(kern, s, num_sms));
         const long block = std::max(mr_stage(T) / 84, std::max(340, 2000 / stages));
         const long cost = r * (8000 + 9 * s * T) + std::max(r * rounds(kb, s) * block,
                                                             std::max(n * kb * mr_stage(T) / 9000, nw * kb * MM_TILE / 3400));
@@ -1341,10 +1343,10 @@ template <bool WMN, int EPI>
 static int mm_launch_rows(const MmOperand* A, const MmOperand* B, int n_ops_a, int n_ops_b, MmParams p, MmShape s,
                           cudaStream_t st) {
   MmMaps maps;   // (a: the weights)
-  for (int i = 0; i < 2; ++i) {
-    if (!mm_map(&maps.a[i], B[i < n_ops_b ? i : 0], WMN, EPI == MM_GATE ? 64 : 128)) return -2;
-    if (!mm_map(&maps.b[i], A[i < n_ops_a ? i : 0], false, s.T)) return -2;
-  }
+  for (int i = 0; i < n_ops_b; ++i)
+    if (!mm_map(&maps.a[i], B[i], WMN, EPI == MM_GATE ? 64 : 128)) return -2;
+  for (int i = 0; i < n_ops_a; ++i)
+    if (!mm_map(&maps.b[i], A[i], false, s.T)) return -2;
   const unsigned tiles = static_cast<unsigned>((p.N[0] + (EPI == MM_GATE ? 63 : 127)) / (EPI == MM_GATE ? 64 : 128) *
                                                ((p.M[0] + s.T - 1) / s.T));
   launch_pdl(mm_rows_kernel<WMN, EPI>, dim3(tiles * s.S), dim3(MM_THREADS), mr_smem(s.T, s.stages), st, s.S, maps, p,
@@ -1364,10 +1366,10 @@ static int mm_launch(const MmOperand* A, const MmOperand* B, int n_ops_a, int n_
   if constexpr (!AMN)
     if (shape.rows) return mm_launch_rows<BMN, EPI>(A, B, n_ops_a, n_ops_b, p, shape, st);
   MmMaps maps;
-  for (int i = 0; i < MM_MAX_PROB; ++i) {
-    if (!mm_map(&maps.a[i], A[i < n_ops_a ? i : 0], AMN, 128)) return -2;
-    if (!mm_map(&maps.b[i], B[i < n_ops_b ? i : 0], BMN, shape.bn / 2)) return -2;
-  }
+  for (int i = 0; i < n_ops_a; ++i)
+    if (!mm_map(&maps.a[i], A[i], AMN, 128)) return -2;
+  for (int i = 0; i < n_ops_b; ++i)
+    if (!mm_map(&maps.b[i], B[i], BMN, shape.bn / 2)) return -2;
   p.bn = shape.bn;
   const long tiles = mm_count_tiles(p, 256, shape.bn / W_DIV);
   if (shape.S > 1) {

@@ -662,7 +662,8 @@ def qi_gated_ffn_forward(ctx: Context, w: qi_gated_ffn, x: torch.Tensor,
     y, yp, ldy = _out(ctx, y, "y", M, H, x, stream)
     if save and gate_up is None:
         gate_up = _new((M, 2 * w.mlp), x, stream, torch.float32)
-    _whole(gate_up, "gate_up", (M, 2 * w.mlp), x, torch.float32)
+    elif gate_up is not None:
+        _whole(gate_up, "gate_up", (M, 2 * w.mlp), x, torch.float32)
     if workspace is None:
         workspace = _new(qi_gated_ffn_workspace_bytes(w, M), x, stream, torch.uint8)
     check(lib().qi_gated_ffn_forward(ctx.handle, C.byref(w), xp, M, ldx, rp, ldr, yp, ldy,
@@ -679,33 +680,38 @@ def qi_gated_ffn_backward(ctx: Context, w: qi_gated_ffn, x: torch.Tensor, dy: to
     in `want` are not computed and come back as None."""
     st = _on(ctx, stream)
     M, H, F = x.shape[0], w.hidden, w.mlp
+    xp, ldx = _rows(ctx, x, "x", H)
+    dp, ldd = _rows(ctx, dy, "dy", H)
     if dy.shape[0] != M:
         raise ValueError("x and dy must have the same number of rows")
     _whole(gate_up, "gate_up", (M, 2 * F), x, torch.float32)
-    if not set(want) <= {"dx", "dgate", "dup", "ddown"}:
-        raise ValueError(f"want names dx, dgate, dup, ddown, not {want}")
-    out = {}
-    for name, t, shape in (("dx", dx, (M, H)), ("dgate", dgate, (F, H)), ("dup", dup, (F, H)),
-                           ("ddown", ddown, (H, F))):
+    op, ldo, found = None, 0, 0
+    if "dx" in want:
+        dx, op, ldo = _out(ctx, dx, "dx", M, H, x, stream)
+        found = 1
+    else:
+        dx = None
+    grads = [dgate, dup, ddown]
+    weights = getattr(w, "_keep", None) if stream is None else None
+    for i, name in enumerate(("dgate", "dup", "ddown")):
         if name not in want:
-            out[name] = None
+            grads[i] = None
             continue
-        if t is None:
-            t = _new(shape, x, stream)
-        if name != "dx":
-            _whole(t, name, shape, x)
-        elif t.shape[0] != M:
-            raise ValueError("x and dx must have the same number of rows")
-        out[name] = t
+        found += 1
+        if grads[i] is not None:
+            _whole(grads[i], name, (H, F) if i == 2 else (F, H), x)
+        elif weights is not None:
+            grads[i] = torch.empty_like(weights[i])
+        else:
+            grads[i] = _new((H, F) if i == 2 else (F, H), x, stream)
+    if found != len(want):
+        raise ValueError(f"want names dx, dgate, dup, ddown, not {want}")
     if workspace is None:
         workspace = _new(qi_gated_ffn_workspace_bytes(w, M, True), x, stream, torch.uint8)
-    xp, ldx = _rows(ctx, x, "x", H)
-    dp, ldd = _rows(ctx, dy, "dy", H)
-    op, ldo = _rows(ctx, out["dx"], "dx", H)
     check(lib().qi_gated_ffn_backward(ctx.handle, C.byref(w), xp, M, ldx, dp, ldd, ptr(gate_up), op,
-                                      ldo, ptr(out["dgate"]), ptr(out["dup"]), ptr(out["ddown"]),
+                                      ldo, ptr(grads[0]), ptr(grads[1]), ptr(grads[2]),
                                       *_scratch(workspace, x), st))
-    return out["dx"], out["dgate"], out["dup"], out["ddown"]
+    return dx, grads[0], grads[1], grads[2]
 
 
 def dims_struct(hidden, heads, mlp, patch, blocks, eps=1e-6) -> qi_dims:

@@ -401,6 +401,17 @@ def test_linear_in_place_strided_and_zero_rows(ctx, M):
     assert same_bits(y[:M], want) and same_bits(y[M:], before[M:])
 
 
+def test_linear_bits_do_not_depend_on_earlier_calls(ctx):
+    """The choice of kernel goes by the sizes alone: a product gives the same bits
+    before and after others of its kind."""
+    sizes = [(64, 4096, 4096), (40, 520, 4096), (200, 2048, 2048), (300, 1024, 2816), (600, 1500, 1024)]
+    ops = [(rand(M, k), qi.bf16_struct(rand(n, k, seed=1, scale=0.02))) for M, n, k in sizes]
+    first = [qi.qi_linear_act(ctx, a, w) for a, w in ops]
+    again = [qi.qi_linear_act(ctx, a, w) for a, w in reversed(ops)][::-1]
+    ctx.check()
+    assert all(same_bits(x, y) for x, y in zip(first, again))
+
+
 def test_linear_activations_at_the_ends(ctx):
     """Large values of both signs: the activations reach x and 0, not NaN."""
     x = torch.tensor([0.0, -0.0, 1e-3, 8.0, -8.0, 40.0, -40.0, 100.0, -100.0, 3e4, -3e4, 1e30, -1e30, 3e38, -3e38],
