@@ -82,13 +82,28 @@ struct MmCfg {
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
-// Execution barrier of a cluster that orders no memory: at the end of a kernel
-// the CTAs only wait for each other's reads, and a releasing arrive would wait
-// for this CTA's output stores too (0.3 us).
+// Execution barrier of a cluster that orders no memory, for the end of a kernel
+// whose CTAs have no access to each other's shared memory left on its way: every
+// remote load has its value, every remote arrival (of a thread or of a commit)
+// has been waited for by the CTA it goes to.  (A releasing arrive would wait for
+// this CTA's output stores too, 0.3 us.)
 __device__ __forceinline__ void cluster_sync_end() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
   __syncwarp();
+}
+
+// Before it ends, a producer waits for the commits that free its last stages:
+// those of a pair arrive from the other CTA, and where the MMA warp gave up the
+// loads may still be on their way.  (They precede the commit that ends the
+// sums, so this takes no time.)
+__device__ __forceinline__ bool mm_stages_free(uint64_t* empty, int stages, int stage, uint32_t phase, int* status) {
+#pragma unroll 1
+  for (int i = 0; i < stages; ++i) {
+    if (!mbar_wait_warp(&empty[stage], phase ^ 1u, status)) return false;
+    if (++stage == stages) { stage = 0; phase ^= 1u; }
+  }
+  return true;
 }
 
 // ---------------------------------------------------------------- activations
@@ -290,7 +305,8 @@ __device__ __forceinline__ void mm_fetch(const MmMaps& maps, MmStage& s, int row
 
 // One accumulator tile of the persistent kernel: rows m0 .. m0 + 127 of this
 // CTA, output columns from n0.  Signals the accumulator buffer free after this
-// warp's last TMEM read.  A thread holds one row, so its own accesses would be
+// warp's last TMEM read if a later tile takes it (reused): an arrival that
+// nobody waits for could reach the even CTA after its exit.  A thread holds one row, so its own accesses would be
 // 16 bytes in each of 32 rows, 32 passes of the load/store unit each; instead a
 // warp's 32 x 32 chunk goes through shared memory and TMA brings the inputs and
 // takes the outputs (TMA keeps to the rows and columns that exist).  TMA needs
@@ -301,7 +317,7 @@ __device__ __forceinline__ void mm_fetch(const MmMaps& maps, MmStage& s, int row
 template <int EPI>
 __device__ __forceinline__ bool mm_epilogue(const MmMaps& maps, const MmParams& p, int pr, uint64_t* tfull,
                                             uint32_t tfull_phase, uint32_t tacc, int m0, int n0, int quarter,
-                                            int half, int lane, uint32_t tempty_addr, MmStage& s, int W) {
+                                            int half, int lane, bool reused, uint32_t tempty_addr, MmStage& s, int W) {
   const int CH = W / 32;   // (W: output columns of a tile)
   const int row0 = m0 + quarter * 32, N = p.N[pr];
   const bool vec = EPI != MM_LINEAR || p.vec;
@@ -329,7 +345,7 @@ __device__ __forceinline__ bool mm_epilogue(const MmMaps& maps, const MmParams& 
     if (c + 2 >= CH) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mm_tempty_signal(tempty_addr);
+      if (reused && lane == 0) mm_tempty_signal(tempty_addr);
     }
     const int col0 = n0 + c * 32;
     if (!rows_in || col0 >= N) continue;
@@ -566,11 +582,11 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   pdl_wait();
   pdl_trigger();
 
+  bool ok = true;
   if (warp == 0) {
     // ------------------------------------------------------------ producer (the whole warp, one lane issues)
     int stage = 0;
     uint32_t phase = 0;
-    bool ok = true;
     for (int tile = worker; tile < num_tiles && ok; tile += workers) {
       int pr, mt, nt;
       mm_tile<256>(p, tile, W, pr, mt, nt);
@@ -590,6 +606,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
         }
       }
     }
+    if (ok) ok = mm_stages_free(empty, STAGES, stage, phase, p.status);
     if (!ok) {
       // Error path: the loads in flight must land before the CTA exits.  The
       // even CTA, which armed the full barriers, waits (bounded) on them; the
@@ -619,7 +636,6 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
-      bool ok = true;
       for (int tile = worker; tile < num_tiles && ok; tile += workers) {
         int pr, mt, nt;
         mm_tile<256>(p, tile, W, pr, mt, nt);
@@ -659,9 +675,11 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
       int pr, mt, nt;
       mm_tile<256>(p, tile, W, pr, mt, nt);
       if (!mm_epilogue<EPI>(maps, p, pr, &tfull[acc], acc_phase, tmem_base + static_cast<uint32_t>(acc * MM_BN),
-                            mt * 256 + rank * 128, nt * W, quarter, half, lane,
-                            mapa_shared(smem_u32(&tempty[acc]), 0), stage, W))
+                            mt * 256 + rank * 128, nt * W, quarter, half, lane, tile + 2 * workers < num_tiles,
+                            mapa_shared(smem_u32(&tempty[acc]), 0), stage, W)) {
+        ok = false;
         break;
+      }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
@@ -669,9 +687,13 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
   }
 
   // Neither CTA of a pair leaves (or frees TMEM) while the other may still read
-  // its shared memory, arrive on its barriers, or have MMAs writing its TMEM.
+  // its shared memory, arrive on its barriers, or have MMAs writing its TMEM:
+  // the MMA warp has waited for every arrival on tempty, the producers for the
+  // last stages.  Behind a wait that ran out arrivals may be left, and the
+  // barrier releases them.
   tc_fence_before();
-  cluster_sync_end();
+  if (ok) cluster_sync_end();
+  else cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 2 * MM_BN);
@@ -764,6 +786,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
       mm_load<true, BMN>(&maps.b[EPI == MM_GATE ? rank : pr + seg], fb, sB + stage * MM_TILE, k, n0);
       if (++stage == STAGES) { stage = 0; phase ^= 1u; }
     }
+    if (ok) ok = mm_stages_free(empty, STAGES, stage, phase, p.status);
     if (!ok) {   // the loads in flight must land before the CTA exits (see mm_kernel)
       if (rank == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -838,7 +861,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1)
     for (int item = threadIdx.x - 64; item < 128 * ng; item += 256) {
       const int c = part * (W / S) + ((item >> 3) & (ng - 1)) * 8;
       const int row = ((item >> 3) / ng) * 8 + (item & 7);
-      if (m0 + row >= p.M[pr]) continue;
+      if (m0 + row >= p.M[pr] || nt * W + c >= p.N[pr]) continue;   // (no load whose value nobody takes)
       const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(row) * 16;
       float v[8], u[8];
 #pragma unroll
@@ -949,6 +972,7 @@ __global__ void __launch_bounds__(MM_THREADS, 2)
       mm_load<false, false>(&maps.b[seg], fb, dst + MM_TILE, k, m0);
       if (++stage == stages) { stage = 0; phase ^= 1u; }
     }
+    if (ok) ok = mm_stages_free(empty, stages, stage, phase, p.status);
     if (!ok) {   // the loads in flight must land before the CTA exits
       for (int s = 0; s < stages; ++s) {
         const uint32_t par = (s < stage) ? phase : (phase ^ 1u);
@@ -1011,6 +1035,7 @@ __global__ void __launch_bounds__(MM_THREADS, 2)
     for (int item = threadIdx.x - 64;; item += 256) {
       const int m = part + S * (item / NG), g = item % NG;
       if (m >= rows) break;
+      if (n0 + g * 8 >= p.N[0]) continue;   // (no load whose value nobody takes)
       float v[8], u[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.f;

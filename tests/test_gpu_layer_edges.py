@@ -1,0 +1,54 @@
+"""Calls of the prompt-encoder layer operators at their edges, against 64-bit
+formulas.  Tolerances count roundings with u = 2^-8, half a bf16 step relative
+to the value, as in the tests of the shapes."""
+import numpy as np
+import pytest
+import torch
+
+from diffusion_transformer_text_dit_b200 import qi
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -8
+BF = torch.bfloat16
+
+
+def rand(*shape, seed=0, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed * 7919 + sum(shape))
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(BF)
+
+
+def same_bits(a, b):
+    """Equal bit patterns (NaN equal to itself, unlike torch.equal)."""
+    assert a.dtype == b.dtype
+    return torch.equal(a.contiguous().view(torch.int16), b.contiguous().view(torch.int16))
+
+
+def acc_tol(a, b):
+    """fp32 sum of a @ b^T (64-bit inputs): the tensor core adds 16 products at a
+    time, k / 16 + 2 sums rounded by 2^-23 of the absolute values at most; times
+    1.13, the largest slope of the activations."""
+    return 1.13 * (a.shape[1] / 16 + 2) * 2.0 ** -23 * (a.abs() @ b.abs().T)
+
+
+@pytest.mark.parametrize("M", [1025, 1100, 1152, 1153, 1280])
+@pytest.mark.parametrize("n", [2304, 12000])
+def test_products_that_follow_each_other_closely(ctx, M, n):
+    """Products of one and of several tiles per pair of CTAs, whose last 128 rows
+    exist or not, each started while the one before it ends: every one gives the
+    bits it gives alone."""
+    k = 1032
+    ops = [(rand(M, k, seed=i), qi.bf16_struct(rand(n, k, seed=10 + i, scale=0.05), rand(n, seed=20 + i)))
+           for i in range(3)]
+    alone = []
+    for a, w in ops:
+        alone.append(qi.qi_linear_act(ctx, a, w, qi.QI_ACT_SILU))
+        torch.cuda.synchronize()
+    a, w = ops[0][0].double(), ops[0][1]._keep[0].double()
+    ref = a @ w.T + ops[0][1]._keep[1].double()
+    ref = ref * torch.sigmoid(ref)
+    # (2^-16: the activation's own evaluation in fp32)
+    assert ((alone[0].double() - ref).abs() <= acc_tol(a, w) + (U + 2.0 ** -16) * ref.abs()).all()
+    outs = [[qi.qi_linear_act(ctx, x, y, qi.QI_ACT_SILU) for x, y in ops] for _ in range(8)]
+    ctx.check()
+    for got in outs:
+        assert all(same_bits(x, y) for x, y in zip(got, alone))
