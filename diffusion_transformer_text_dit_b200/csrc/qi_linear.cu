@@ -122,7 +122,8 @@ __device__ __forceinline__ float act_f(float x, int act) {
 
 // act(x) and act'(x).  SiLU: x s, s (1 + x (1 - s)) with s = logistic(x).
 // GELU-tanh, written x s with s = logistic(2z), z = k0 (x + k1 x^3):
-// act' = s + x s (1 - s) 2 k0 (1 + 3 k1 x^2).
+// act' = s + x s (1 - s) 2 k0 (1 + 3 k1 x^2); s (1 - s) is 0 long before |x| = 100,
+// and x^2 stops there, so that the product is 0 where x^2 would be infinite.
 __device__ __forceinline__ void act_grad_f(float x, int act, float& a, float& da) {
   if (act == ACT_SILU) {
     const float s = logistic_f(x);
@@ -133,7 +134,7 @@ __device__ __forceinline__ void act_grad_f(float x, int act, float& a, float& da
     const float x2 = x * x;
     const float s = logistic_f(2.0f * k0 * fmaf(k1 * x, x2, x));
     a = x * s;
-    da = fmaf(x * s * (1.0f - s), 2.0f * k0 * fmaf(3.0f * k1, x2, 1.0f), s);
+    da = fmaf(x * s * (1.0f - s), 2.0f * k0 * fmaf(3.0f * k1, fminf(x2, 1e4f), 1.0f), s);
   }
 }
 

@@ -52,3 +52,38 @@ def test_products_that_follow_each_other_closely(ctx, M, n):
     ctx.check()
     for got in outs:
         assert all(same_bits(x, y) for x, y in zip(got, alone))
+
+
+def act64(x, act):
+    if act == qi.QI_ACT_SILU:
+        return x * torch.sigmoid(x)
+    # 0.5 (1 + tanh z) = logistic(2 z), without the cancellation of 1 + tanh z at z << 0
+    return x * torch.sigmoid(2 * (2 / np.pi) ** 0.5 * (x + 0.044715 * x ** 3))
+
+
+@pytest.mark.parametrize("act", [qi.QI_ACT_SILU, qi.QI_ACT_GELU_TANH])
+@pytest.mark.parametrize("M", [1, 40, 1300])
+def test_gated_ffn_gradients_at_the_ends(ctx, M, act):
+    """Gate values of both signs up to the largest: the activation's derivative goes to
+    1 and 0, not to NaN.  Row 0 of dy and x and the weights pick act(g) and act'(g)
+    out of the sums: one term each, the rest 0.  One rounding to bf16 (the output
+    repeats it exactly) and 2^-15 for the evaluation in fp32 (two terms)."""
+    ends = [0.0, 1e-3, 8.0, 40.0, 100.0, 3e4, 1.8e19, 2e19, 1e30, 3e38]
+    g = torch.tensor([s * v for v in ends for s in (1.0, -1.0)] + [0.5, -0.5, 3.0, -3.0], device="cuda")
+    F = H = len(g)
+    up = torch.zeros(F, H, dtype=BF, device="cuda")
+    gate = torch.eye(F, dtype=BF, device="cuda")
+    down = torch.zeros(H, F, dtype=BF, device="cuda")
+    down[0] = 1
+    x, dy = (torch.zeros(M, H, dtype=BF, device="cuda") for _ in range(2))
+    x[0, 0] = dy[0, 0] = 1
+    gate_up = torch.cat([g, torch.ones_like(g)]).repeat(M, 1)
+    dx, dgate, dup, ddown = qi.qi_gated_ffn_backward(ctx, qi.gated_ffn_struct(gate, up, down, act), x, dy, gate_up)
+    ctx.check()
+    at = g.double().requires_grad_(True)
+    value = act64(at, act)
+    slope = torch.autograd.grad(value.sum(), at)[0]
+    for got, ref in ((dx[0], slope), (dgate[:, 0], slope), (dup[:, 0], value), (ddown[0], value)):
+        ref = ref.detach()
+        assert torch.isfinite(got).all()
+        assert ((got.double() - ref).abs() <= (U + 2.0 ** -15) * ref.abs() + 1e-30).all()
