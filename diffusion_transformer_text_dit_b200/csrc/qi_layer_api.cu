@@ -130,10 +130,9 @@ int qi_attn_causal_packed(qi_ctx* ctx, const uint16_t* q, int ldq, int q_rows, c
       (r = check_rows("k", k, kv_heads * 128, ldk, k_rows > 0)) ||
       (r = check_rows("v", v, kv_heads * 128, ldv, k_rows > 0)))
     return r;
-  const size_t ob = span_bytes(q_rows, heads * 128, ldo), kb = span_bytes(k_rows, kv_heads * 128, ldk),
-               vb = span_bytes(k_rows, kv_heads * 128, ldv);
-  if (overlap(o, ob, k, kb) || overlap(o, ob, v, vb) ||
-      overlap(o, ob, q, span_bytes(q_rows, heads * 128, ldq)))
+  const size_t qb = span_bytes(q_rows, heads * 128, ldq), ob = span_bytes(q_rows, heads * 128, ldo),
+               kb = span_bytes(k_rows, kv_heads * 128, ldk), vb = span_bytes(k_rows, kv_heads * 128, ldv);
+  if (overlap(o, ob, k, kb) || overlap(o, ob, v, vb) || overlap(o, ob, q, qb))
     return fail(QI_ERR_INVALID_ARG, "o overlaps q, k or v");
   qi::PackedPlan tile, token;
   qi::packed_plan(spans, n_seqs, heads, kv_heads, ctx->num_sms, &tile, &token);
@@ -143,6 +142,9 @@ int qi_attn_causal_packed(qi_ctx* ctx, const uint16_t* q, int ldq, int q_rows, c
       return fail(QI_ERR_WORKSPACE, "packed attention needs %zu bytes of workspace, got %zu", need,
                   workspace ? workspace_bytes : static_cast<size_t>(0));
     if (!aligned16(workspace)) return fail(QI_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+    if (overlap(workspace, need, q, qb) || overlap(workspace, need, k, kb) || overlap(workspace, need, v, vb) ||
+        overlap(workspace, need, o, ob))
+      return fail(QI_ERR_INVALID_ARG, "the workspace overlaps q, k, v or o");
   }
   if (tile.units == 0 && token.units == 0) return QI_OK;
   qi::PackedAttnParams p;
@@ -187,6 +189,7 @@ int qi_linear_act(qi_ctx* ctx, const uint16_t* a, int M, int lda, const qi_linea
     return fail(QI_ERR_INVALID_ARG, "leading dimension of y or residual < n");
   const size_t yb = span_bytes(M, w->n, ldy);
   if (overlap(y, yb, a, span_bytes(M, w->k, lda)) || overlap(y, yb, w->w, span_bytes(w->n, w->k, w->k)) ||
+      overlap(y, yb, w->bias, static_cast<size_t>(w->n) * 2) ||
       (residual && (residual != y || ld_residual != ldy) &&
        overlap(y, yb, residual, span_bytes(M, w->n, ld_residual))))
     return fail(QI_ERR_INVALID_ARG, "y overlaps an input (only residual == y with the same ld is allowed)");

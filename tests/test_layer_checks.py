@@ -1,0 +1,70 @@
+"""Further refusals of the prompt-encoder layer calls, on the host and before
+anything is launched.  Run without a GPU: the calls get a zeroed stand-in for a
+context (of which a check reads the SM count only) and pointers that nothing
+may follow."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+from diffusion_transformer_text_dit_b200 import build_lib, qi
+
+P = 1 << 20            # a 16-byte aligned address for pointers that must not be read
+INV, SHAPE, ALIGN, WS = (qi.QI_ERR_INVALID_ARG, qi.QI_ERR_UNSUPPORTED_SHAPE, qi.QI_ERR_ALIGNMENT,
+                         qi.QI_ERR_WORKSPACE)
+
+
+@pytest.fixture(scope="module")
+def L():
+    build_lib.build()
+    return qi.lib()
+
+
+@pytest.fixture(scope="module")
+def dummy():
+    """Zeroed memory in the place of a context: device 0, 148 SMs."""
+    buf = (C.c_int32 * 4096)()
+    buf[1] = 148
+    return buf
+
+
+def attn(L, ctx, spans, **kw):
+    t = np.asarray(spans, np.int32).reshape(-1, 4)
+    a = dict(q=16 * P, ldq=512, q_rows=16, k=32 * P, ldk=256, v=48 * P, ldv=256, k_rows=8192, heads=4,
+             kv_heads=2, scale=0.1, o=64 * P, ldo=512, ws=None, ws_bytes=0)
+    a.update(kw)
+    return L.qi_attn_causal_packed(C.addressof(ctx), a["q"], a["ldq"], a["q_rows"], a["k"], a["ldk"], a["v"],
+                                   a["ldv"], a["k_rows"], a["heads"], a["kv_heads"], 128, t.ctypes.data, len(t),
+                                   a["scale"], a["o"], a["ldo"], a["ws"], a["ws_bytes"], None)
+
+
+def linear(L, ctx, **kw):
+    a = dict(a=P, M=4, lda=64, w=2 * P, bias=None, n=40, k=64, act=0, res=None, ldr=0, y=3 * P, ldy=40)
+    a.update(kw)
+    w = qi.qi_linear_bf16()
+    w.w, w.bias, w.n, w.k = a["w"], a["bias"], a["n"], a["k"]
+    return L.qi_linear_act(C.addressof(ctx), a["a"], a["M"], a["lda"], C.byref(w), a["act"], a["res"], a["ldr"],
+                           a["y"], a["ldy"], None)
+
+
+def refused(got, code, text):
+    """The code, and that the check in question gave it."""
+    return got == code and text in qi.last_error()
+
+
+@pytest.mark.parametrize("at", ["q", "k", "v", "o"])
+@pytest.mark.parametrize("end", [False, True])
+def test_attention_workspace_over_a_buffer(L, dummy, at, end):
+    """Partial results over q, k, v or o: refused whether the workspace begins in the
+    buffer or the buffer in the last bytes of the workspace."""
+    t = np.array([[0, 1, 0, 8192]], np.int32)
+    n = C.c_size_t()
+    assert L.qi_attn_causal_packed_workspace_bytes(C.addressof(dummy), t.ctypes.data, 1, 4, 2, C.byref(n)) == qi.QI_OK
+    base = dict(q=16 * P, k=32 * P, v=48 * P, o=64 * P)[at]
+    ws = base - n.value + 16 if end else base + 128
+    assert refused(attn(L, dummy, t, ws=ws, ws_bytes=n.value), INV, "workspace overlaps")
+
+
+def test_linear_output_over_the_bias(L, dummy):
+    for bias in (3 * P, 3 * P + 304, 3 * P - 64):
+        assert refused(linear(L, dummy, bias=bias), INV, "y overlaps")
