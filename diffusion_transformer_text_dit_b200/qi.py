@@ -359,7 +359,17 @@ def w8_struct(q, s, rowsum, bias=None) -> qi_w8:
     return w
 
 
+_BF16_BITS = (torch.bfloat16, torch.uint16, torch.int16)   # bf16, or its bit patterns
+
+
 def bf16_struct(w, bias=None) -> qi_linear_bf16:
+    """A BF16 Linear: w [n, k], bias [n] or None."""
+    if w.dim() != 2 or w.dtype not in _BF16_BITS:
+        raise ValueError(f"the weight of a BF16 Linear must be a 2-D bf16 tensor, not {w.dtype} {list(w.shape)}")
+    if bias is not None and (bias.dtype not in _BF16_BITS or bias.numel() != w.shape[0]
+                             or bias.device != w.device):
+        raise ValueError(f"the bias must be {w.shape[0]} bf16 values on the weight's device, not {bias.dtype} "
+                         f"{list(bias.shape)} on {bias.device}")
     s = qi_linear_bf16()
     s.w, s.bias = ptr(w), ptr(bias)
     s.n, s.k = w.shape
@@ -524,6 +534,14 @@ def _rows(ctx: Context, t: Optional[torch.Tensor], name: str, cols: int):
     return t.data_ptr(), ld
 
 
+def _weights_here(ctx: Context, w):
+    """Checks that the tensors behind a weight struct are on the context's device
+    (a struct's maker has checked that they are all on one)."""
+    keep = getattr(w, "_keep", None)
+    if keep is not None and keep[0].get_device() != ctx.device:
+        raise ValueError(f"the weights must be on cuda:{ctx.device}, not {keep[0].device}")
+
+
 def _whole(t: Optional[torch.Tensor], name: str, shape, like: torch.Tensor, dtype=torch.bfloat16):
     """Checks a contiguous tensor of a given shape on the device of `like`."""
     if t is not None and (tuple(t.shape) != shape or t.dtype != dtype or t.device != like.device
@@ -616,6 +634,7 @@ def qi_linear_act(ctx: Context, a: torch.Tensor, w: qi_linear_bf16, act: int = Q
                   residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
                   stream=None):
     """y = act(a w^T + bias) + residual, bf16 (residual may be y)."""
+    _weights_here(ctx, w)
     st = _on(ctx, stream)
     ap, lda = _rows(ctx, a, "a", w.k)
     M, n = a.shape[0], w.n
@@ -635,6 +654,8 @@ def gated_ffn_struct(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
         raise ValueError("gate and up must be [mlp, hidden], down [hidden, mlp]")
     if any(t.dtype != torch.bfloat16 for t in (gate, up, down)):
         raise ValueError("gated ffn weights must be bf16")
+    if up.device != gate.device or down.device != gate.device:
+        raise ValueError("gated ffn weights must be on one device")
     s = qi_gated_ffn()
     s.gate, s.up, s.down, s.hidden, s.mlp, s.act = ptr(gate), ptr(up), ptr(down), H, F, act
     s._keep = (gate, up, down)
@@ -653,6 +674,7 @@ def qi_gated_ffn_forward(ctx: Context, w: qi_gated_ffn, x: torch.Tensor,
                          workspace: Optional[torch.Tensor] = None, stream=None):
     """y = (act(x gate^T) * (x up^T)) down^T + residual.  save=True (or a gate_up
     buffer [M, 2 mlp] fp32) also returns what the backward call needs: (y, gate_up)."""
+    _weights_here(ctx, w)
     st = _on(ctx, stream)
     M, H = x.shape[0], w.hidden
     xp, ldx = _rows(ctx, x, "x", H)
@@ -678,6 +700,7 @@ def qi_gated_ffn_backward(ctx: Context, w: qi_gated_ffn, x: torch.Tensor, dy: to
                           workspace: Optional[torch.Tensor] = None, stream=None):
     """(dx, dgate, dup, ddown) of the block for the output gradient dy; gradients not
     in `want` are not computed and come back as None."""
+    _weights_here(ctx, w)
     st = _on(ctx, stream)
     M, H, F = x.shape[0], w.hidden, w.mlp
     xp, ldx = _rows(ctx, x, "x", H)

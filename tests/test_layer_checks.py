@@ -6,6 +6,7 @@ import ctypes as C
 
 import numpy as np
 import pytest
+import torch
 
 from diffusion_transformer_text_dit_b200 import build_lib, qi
 
@@ -68,3 +69,50 @@ def test_attention_workspace_over_a_buffer(L, dummy, at, end):
 def test_linear_output_over_the_bias(L, dummy):
     for bias in (3 * P, 3 * P + 304, 3 * P - 64):
         assert refused(linear(L, dummy, bias=bias), INV, "y overlaps")
+
+
+# ------------------------------------------------------------------ binding
+
+def zeros(*shape, dtype=torch.bfloat16, device="cpu"):
+    return torch.zeros(*shape, dtype=dtype, device=device)
+
+
+@pytest.mark.parametrize("w,bias,text", [
+    (zeros(4, 8, dtype=torch.float16), None, "weight"), (zeros(4, 8, dtype=torch.float32), None, "weight"),
+    (zeros(4), None, "weight"), (zeros(4, 8), zeros(3), "bias"), (zeros(4, 8), zeros(8), "bias"),
+    (zeros(4, 8), zeros(4, dtype=torch.float32), "bias"), (zeros(4, 8), zeros(4, device="meta"), "bias"),
+])
+def test_linear_weights_are_checked(w, bias, text):
+    """A weight that is not bf16, a bias that is not, or is shorter than the output."""
+    with pytest.raises(ValueError, match=text):
+        qi.bf16_struct(w, bias)
+
+
+def test_linear_weights_that_are_right_get_past_the_checks():
+    for w, bias in ((zeros(4, 8), None), (zeros(4, 8), zeros(4)), (zeros(4, 8, dtype=torch.int16), zeros(4))):
+        with pytest.raises(ValueError, match="takes CUDA tensors"):   # (host tensors: refused behind them)
+            qi.bf16_struct(w, bias)
+
+
+def test_gated_ffn_weights_on_two_devices():
+    with pytest.raises(ValueError, match="one device"):
+        qi.gated_ffn_struct(zeros(16, 8), zeros(16, 8, device="meta"), zeros(8, 16))
+
+
+def test_weights_on_another_device_than_the_context():
+    """Activations are checked against the context's device; so are the weights."""
+    class Ctx:
+        device, handle = 0, None
+
+    class Stream:
+        cuda_stream = 0
+
+    lin, ffn = qi.qi_linear_bf16(), qi.qi_gated_ffn()
+    lin.n, lin.k, ffn.hidden, ffn.mlp = 4, 8, 8, 16
+    lin._keep, ffn._keep = (zeros(4, 8), None), (zeros(16, 8), zeros(16, 8), zeros(8, 16))
+    x, gu = zeros(2, 8), zeros(2, 32, dtype=torch.float32)
+    for call in (lambda: qi.qi_linear_act(Ctx, x, lin, stream=Stream),
+                 lambda: qi.qi_gated_ffn_forward(Ctx, ffn, x, stream=Stream),
+                 lambda: qi.qi_gated_ffn_backward(Ctx, ffn, x, x, gu, stream=Stream)):
+        with pytest.raises(ValueError, match="weights"):
+            call()
