@@ -9,6 +9,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "qi_host.h"
@@ -166,8 +167,10 @@ StepBufs carve_step(Carve& c, const qi_dims& d, int Sq, int S, bool own_kv) {
 
 namespace qi {
 
+// The driver's encoder, asked for by the first call (several threads may make it).
 static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 encode = known.load(std::memory_order_acquire);
   if (!encode) {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -176,6 +179,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
         q != cudaDriverEntryPointSuccess || !fn)
       return nullptr;
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    known.store(encode, std::memory_order_release);
   }
   return encode;
 }

@@ -1,6 +1,10 @@
 """Calls of the prompt-encoder layer operators at their edges, against 64-bit
 formulas.  Tolerances count roundings with u = 2^-8, half a bf16 step relative
 to the value, as in the tests of the shapes."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -87,3 +91,50 @@ def test_gated_ffn_gradients_at_the_ends(ctx, M, act):
         ref = ref.detach()
         assert torch.isfinite(got).all()
         assert ((got.double() - ref).abs() <= (U + 2.0 ** -15) * ref.abs() + 1e-30).all()
+
+
+FIRST_CALLS = """
+import threading
+import torch
+from diffusion_transformer_text_dit_b200 import qi
+
+torch.manual_seed(1)
+n = 6
+a, w = (torch.randn(300, 520, device="cuda").bfloat16() for _ in range(2))
+q, k, v = (torch.randn(200, 256, device="cuda").bfloat16() for _ in range(3))
+spans = torch.tensor([[0, 200, 0, 200]], dtype=torch.int32)
+work = [(qi.Context(), torch.cuda.Stream(), torch.empty_like(q), torch.empty(300, 300, device="cuda").bfloat16())
+        for _ in range(n)]
+torch.cuda.synchronize()
+ready, failed = threading.Barrier(n), []
+
+def call(i):
+    c, st, o, y = work[i]
+    ready.wait()
+    try:
+        if i % 2:
+            qi.qi_attn_causal_packed(c, q, k, v, spans, 2, 2, o=o, stream=st)
+        qi.qi_linear_act(c, a, qi.bf16_struct(w), y=y, stream=st)
+        if not i % 2:
+            qi.qi_attn_causal_packed(c, q, k, v, spans, 2, 2, o=o, stream=st)
+        c.check(st)
+    except Exception as e:
+        failed.append(e)
+
+threads = [threading.Thread(target=call, args=(i,)) for i in range(n)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+assert not failed, failed
+bits = lambda t: t.view(torch.int16)
+assert all(torch.equal(bits(x[2]), bits(work[0][2])) and torch.equal(bits(x[3]), bits(work[0][3])) for x in work)
+print("same")
+"""
+
+
+def test_first_calls_from_several_threads(ctx):
+    """The first calls of a process, made at the same time by host threads with a
+    context and a stream each (what the library looks up on first use, it looks up
+    once for all or again with the same answer)."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr
