@@ -185,6 +185,8 @@ int qi_linear_act(qi_ctx* ctx, const uint16_t* a, int M, int lda, const qi_linea
   if ((r = check_act(act, true))) return r;
   if ((r = check_rows("a", a, w->k, lda, M > 0))) return r;
   if (M > 0 && !y) return fail(QI_ERR_INVALID_ARG, "y is NULL");
+  if ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(residual)) & 1)
+    return fail(QI_ERR_ALIGNMENT, "y and residual must be 2-byte aligned");
   if (ldy < w->n || (residual && ld_residual < w->n))
     return fail(QI_ERR_INVALID_ARG, "leading dimension of y or residual < n");
   const size_t yb = span_bytes(M, w->n, ldy);

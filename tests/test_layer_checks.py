@@ -71,6 +71,13 @@ def test_linear_output_over_the_bias(L, dummy):
         assert refused(linear(L, dummy, bias=bias), INV, "y overlaps")
 
 
+def test_linear_rows_at_odd_addresses(L, dummy):
+    """Any row distance is taken, but a bf16 value lies at an even address."""
+    assert refused(linear(L, dummy, y=3 * P + 1), ALIGN, "2-byte")
+    assert refused(linear(L, dummy, res=4 * P + 1, ldr=40), ALIGN, "2-byte")
+    assert refused(linear(L, dummy, y=3 * P + 1, res=3 * P + 1, ldr=40), ALIGN, "2-byte")
+
+
 # ------------------------------------------------------------------ binding
 
 def zeros(*shape, dtype=torch.bfloat16, device="cpu"):
