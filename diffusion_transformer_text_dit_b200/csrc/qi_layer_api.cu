@@ -20,6 +20,10 @@ static_assert(QI_ACT_NONE == qi::ACT_NONE && QI_ACT_GELU_TANH == qi::ACT_GELU_TA
 
 namespace {
 
+// Largest extent of a matrix (rows, columns, K) and length of a sequence: the
+// kernels' indexes, rounded up to whole tiles, stay below 2^31.
+constexpr int MAX_EXTENT = 1 << 30;
+
 // Makes the context's device current for the duration of a call, so that a
 // call works whatever device its thread uses otherwise.
 struct DeviceScope {
@@ -80,14 +84,21 @@ int check_spans(const int32_t* spans, int n, int heads, int kv_heads, long long 
     return fail(QI_ERR_UNSUPPORTED_SHAPE, "at most 128 query heads per key/value head, 4096 heads");
   std::vector<std::pair<long long, long long>> q;
   q.reserve(n);
+  long long keys = 0;
   for (int i = 0; i < n; ++i) {
     const long long q0 = spans[4 * i], ql = spans[4 * i + 1], k0 = spans[4 * i + 2], kl = spans[4 * i + 3];
     if (q0 < 0 || ql < 0 || k0 < 0 || kl < 0)
       return fail(QI_ERR_INVALID_ARG, "sequence %d: negative start or length", i);
     if ((q_rows >= 0 && q0 + ql > q_rows) || (k_rows >= 0 && k0 + kl > k_rows))
       return fail(QI_ERR_INVALID_ARG, "sequence %d: rows outside the q or k buffer", i);
+    if (ql > MAX_EXTENT || kl > MAX_EXTENT)
+      return fail(QI_ERR_UNSUPPORTED_SHAPE, "sequence %d: more than 2^30 queries or keys", i);
     if (ql > 0) q.emplace_back(q0, q0 + ql);
+    keys += kl;
   }
+  // (ranges of 256 keys: units of work stay below 2^31)
+  if (keys * kv_heads >= 1ll << 38)
+    return fail(QI_ERR_UNSUPPORTED_SHAPE, "keys x kv_heads of all sequences must stay below 2^38");
   std::sort(q.begin(), q.end());
   for (size_t i = 1; i < q.size(); ++i)
     if (q[i].first < q[i - 1].second)
@@ -179,6 +190,8 @@ int qi_linear_act(qi_ctx* ctx, const uint16_t* a, int M, int lda, const qi_linea
   if (!ctx || !w || !w->w) return fail(QI_ERR_INVALID_ARG, "NULL argument");
   if (M < 0 || w->n < 1 || w->k < 1) return fail(QI_ERR_INVALID_ARG, "need M >= 0, n >= 1, k >= 1");
   if (w->k % 8 != 0) return fail(QI_ERR_UNSUPPORTED_SHAPE, "k = %d is not a multiple of 8", w->k);
+  if (M > MAX_EXTENT || w->n > MAX_EXTENT || w->k > MAX_EXTENT)
+    return fail(QI_ERR_UNSUPPORTED_SHAPE, "M, n and k must not exceed 2^30");
   if (!aligned16(w->w) || (w->bias && !aligned16(w->bias)))
     return fail(QI_ERR_ALIGNMENT, "weight and bias must be 16-byte aligned");
   int r;
@@ -241,9 +254,17 @@ int check_gated(const qi_gated_ffn* w) {
   if (!w || !w->gate || !w->up || !w->down) return fail(QI_ERR_INVALID_ARG, "gated ffn: NULL weight");
   if (w->hidden < 8 || w->mlp < 8 || w->hidden % 8 != 0 || w->mlp % 8 != 0)
     return fail(QI_ERR_UNSUPPORTED_SHAPE, "gated ffn: hidden and mlp must be positive multiples of 8");
+  if (w->hidden > MAX_EXTENT || w->mlp > MAX_EXTENT / 2)   // (gate | up is one row)
+    return fail(QI_ERR_UNSUPPORTED_SHAPE, "gated ffn: hidden must not exceed 2^30, mlp 2^29");
   if (!aligned16(w->gate) || !aligned16(w->up) || !aligned16(w->down))
     return fail(QI_ERR_ALIGNMENT, "gated ffn: weights must be 16-byte aligned");
   return check_act(w->act, false);
+}
+
+int check_m(int M) {
+  if (M < 0) return fail(QI_ERR_INVALID_ARG, "M must be >= 0");
+  if (M > MAX_EXTENT) return fail(QI_ERR_UNSUPPORTED_SHAPE, "M must not exceed 2^30");
+  return QI_OK;
 }
 
 size_t gated_bytes(const qi_gated_ffn& w, int M, bool backward) {
@@ -268,7 +289,7 @@ int qi_gated_ffn_workspace_bytes(const qi_gated_ffn* w, int M, int backward, siz
   if (!bytes) return fail(QI_ERR_INVALID_ARG, "NULL output");
   int r;
   if ((r = check_gated(w))) return r;
-  if (M < 0) return fail(QI_ERR_INVALID_ARG, "M must be >= 0");
+  if ((r = check_m(M))) return r;
   *bytes = gated_bytes(*w, M, backward != 0);
   return QI_OK;
 }
@@ -279,7 +300,7 @@ int qi_gated_ffn_forward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x, 
   if (!ctx) return fail(QI_ERR_INVALID_ARG, "ctx is NULL");
   int r;
   if ((r = check_gated(w))) return r;
-  if (M < 0) return fail(QI_ERR_INVALID_ARG, "M must be >= 0");
+  if ((r = check_m(M))) return r;
   const int H = w->hidden, F = w->mlp;
   if ((r = check_rows("x", x, H, ldx, M > 0)) || (r = check_rows("y", y, H, ldy, M > 0)) ||
       (r = check_rows("residual", residual, H, ld_residual, false)) ||
@@ -351,7 +372,7 @@ int qi_gated_ffn_backward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x,
   if (!ctx) return fail(QI_ERR_INVALID_ARG, "ctx is NULL");
   int r;
   if ((r = check_gated(w))) return r;
-  if (M < 0) return fail(QI_ERR_INVALID_ARG, "M must be >= 0");
+  if ((r = check_m(M))) return r;
   const int H = w->hidden, F = w->mlp;
   if ((r = check_rows("x", x, H, ldx, M > 0)) || (r = check_rows("dy", dy, H, ld_dy, M > 0)) ||
       (r = check_rows("gate_up", gate_up, 2 * F, 2 * F, M > 0)) ||

@@ -78,6 +78,52 @@ def test_linear_rows_at_odd_addresses(L, dummy):
     assert refused(linear(L, dummy, y=3 * P + 1, res=3 * P + 1, ldr=40), ALIGN, "2-byte")
 
 
+@pytest.mark.parametrize("span,heads,kvh", [((0, 2 ** 31 - 1, 0, 4), 1, 1), ((0, 2 ** 30 + 1, 0, 4), 1, 1),
+                                            ((0, 1, 0, 2 ** 31 - 1), 1, 1), ((0, 1, 0, 2 ** 30), 4096, 4096)])
+def test_attention_sizes_past_the_index_range(L, dummy, span, heads, kvh):
+    """Lengths whose tiles or key ranges would not be counted in 32 bits."""
+    t = np.array([span], np.int32)
+    n = C.c_size_t()
+    c = C.addressof(dummy)
+    assert refused(L.qi_attn_causal_packed_workspace_bytes(c, t.ctypes.data, 1, heads, kvh, C.byref(n)), SHAPE, "2^")
+    rows = 2 ** 31 - 1
+    got = attn(L, dummy, t, heads=heads, kv_heads=kvh, q_rows=rows, k_rows=rows, ldq=heads * 128, ldo=heads * 128,
+               ldk=kvh * 128, ldv=kvh * 128)
+    assert refused(got, SHAPE, "2^")
+
+
+def test_attention_plans_within_the_index_range(L, dummy):
+    """A million keys behind each of many tokens that share them, and the longest prompt."""
+    n = C.c_size_t()
+    for spans, heads, kvh in (([(i, 1, 0, 1 << 20) for i in range(qi.QI_MAX_SEQS)], 64, 8),
+                              ([(0, 1 << 20, 0, 1 << 20)], 32, 8)):
+        t = np.array(spans, np.int32)
+        assert L.qi_attn_causal_packed_workspace_bytes(C.addressof(dummy), t.ctypes.data, len(t), heads, kvh,
+                                                       C.byref(n)) == qi.QI_OK
+        # token ranges of 256 to 512 keys, each a partial result of G rows of 130 fp32 values
+        if len(t) > 1:
+            per_key = qi.QI_MAX_SEQS * heads * 130 * 4
+            assert (1 << 20) // 512 * per_key <= n.value <= (1 << 20) // 256 * per_key
+        else:
+            assert n.value == 0
+
+
+def test_product_sizes_past_the_index_range(L, dummy):
+    big = 2 ** 30 + 8
+    for kw in (dict(M=2 ** 31 - 1), dict(M=big), dict(n=2 ** 31 - 1, ldy=2 ** 31 - 1), dict(n=big, ldy=big),
+               dict(k=big, lda=big)):
+        assert refused(linear(L, dummy, **kw), SHAPE, "2^30")
+    n = C.c_size_t()
+    for hidden, mlp, M in ((big, 16, 4), (64, big // 2 + 4, 4), (64, 128, 2 ** 31 - 1)):
+        w = qi.qi_gated_ffn()
+        w.gate, w.up, w.down, w.hidden, w.mlp, w.act = P, 2 * P, 3 * P, hidden, mlp, qi.QI_ACT_SILU
+        args = [C.addressof(dummy), C.byref(w), 4 * P, M, hidden]
+        assert refused(L.qi_gated_ffn_workspace_bytes(C.byref(w), M, 0, C.byref(n)), SHAPE, "2^")
+        assert refused(L.qi_gated_ffn_forward(*args, None, 0, 5 * P, hidden, None, 6 * P, 1 << 20, None), SHAPE, "2^")
+        assert refused(L.qi_gated_ffn_backward(*args, 5 * P, hidden, 7 * P, None, 0, None, None, None, 6 * P, 1 << 20,
+                                               None), SHAPE, "2^")
+
+
 # ------------------------------------------------------------------ binding
 
 def zeros(*shape, dtype=torch.bfloat16, device="cpu"):
