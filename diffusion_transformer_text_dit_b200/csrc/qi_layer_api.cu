@@ -44,12 +44,29 @@ struct DeviceScope {
 
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + bn && y < x + an;
+  return a && b && an > 0 && bn > 0 && x < y + bn && y < x + an;
 }
 
 // Bytes from the first to the last value of a [rows, cols] matrix of 2-byte values.
 size_t span_bytes(int rows, int cols, int ld) {
   return rows == 0 ? 0 : (static_cast<size_t>(rows - 1) * ld + cols) * 2;
+}
+
+// A [rows, cols] matrix of 2-byte values.
+struct Rows {
+  const void* p;
+  int rows, cols, ld;
+};
+
+// Whether two matrices share a byte.  Column ranges of the same rows (a fused
+// q | k | v | o block) lie between each other without sharing one.
+bool overlap(const Rows& a, const Rows& b) {
+  if (!overlap(a.p, span_bytes(a.rows, a.cols, a.ld), b.p, span_bytes(b.rows, b.cols, b.ld))) return false;
+  const int lda = a.rows == 1 ? std::max(a.cols, b.ld) : a.ld, ldb = b.rows == 1 ? std::max(b.cols, lda) : b.ld;
+  const intptr_t bytes = reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p);
+  if (lda != ldb || bytes % 2 != 0) return true;
+  const intptr_t at = (bytes / 2 % lda + lda) % lda;   // b's first column, counted in a's rows
+  return at < a.cols || at + b.cols > lda;
 }
 
 int check_act(int act, bool none_ok) {
@@ -141,9 +158,9 @@ int qi_attn_causal_packed(qi_ctx* ctx, const uint16_t* q, int ldq, int q_rows, c
       (r = check_rows("k", k, kv_heads * 128, ldk, k_rows > 0)) ||
       (r = check_rows("v", v, kv_heads * 128, ldv, k_rows > 0)))
     return r;
-  const size_t qb = span_bytes(q_rows, heads * 128, ldq), ob = span_bytes(q_rows, heads * 128, ldo),
-               kb = span_bytes(k_rows, kv_heads * 128, ldk), vb = span_bytes(k_rows, kv_heads * 128, ldv);
-  if (overlap(o, ob, k, kb) || overlap(o, ob, v, vb) || overlap(o, ob, q, qb))
+  const Rows qr{q, q_rows, heads * 128, ldq}, orows{o, q_rows, heads * 128, ldo}, kr{k, k_rows, kv_heads * 128, ldk},
+      vr{v, k_rows, kv_heads * 128, ldv};
+  if (overlap(orows, kr) || overlap(orows, vr) || overlap(orows, qr))
     return fail(QI_ERR_INVALID_ARG, "o overlaps q, k or v");
   qi::PackedPlan tile, token;
   qi::packed_plan(spans, n_seqs, heads, kv_heads, ctx->num_sms, &tile, &token);
@@ -153,9 +170,9 @@ int qi_attn_causal_packed(qi_ctx* ctx, const uint16_t* q, int ldq, int q_rows, c
       return fail(QI_ERR_WORKSPACE, "packed attention needs %zu bytes of workspace, got %zu", need,
                   workspace ? workspace_bytes : static_cast<size_t>(0));
     if (!aligned16(workspace)) return fail(QI_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
-    if (overlap(workspace, need, q, qb) || overlap(workspace, need, k, kb) || overlap(workspace, need, v, vb) ||
-        overlap(workspace, need, o, ob))
-      return fail(QI_ERR_INVALID_ARG, "the workspace overlaps q, k, v or o");
+    for (const Rows& r : {qr, kr, vr, orows})
+      if (overlap(workspace, need, r.p, span_bytes(r.rows, r.cols, r.ld)))
+        return fail(QI_ERR_INVALID_ARG, "the workspace overlaps q, k, v or o");
   }
   if (tile.units == 0 && token.units == 0) return QI_OK;
   qi::PackedAttnParams p;
@@ -203,10 +220,10 @@ int qi_linear_act(qi_ctx* ctx, const uint16_t* a, int M, int lda, const qi_linea
   if (ldy < w->n || (residual && ld_residual < w->n))
     return fail(QI_ERR_INVALID_ARG, "leading dimension of y or residual < n");
   const size_t yb = span_bytes(M, w->n, ldy);
-  if (overlap(y, yb, a, span_bytes(M, w->k, lda)) || overlap(y, yb, w->w, span_bytes(w->n, w->k, w->k)) ||
+  const Rows yr{y, M, w->n, ldy};
+  if (overlap(yr, {a, M, w->k, lda}) || overlap(y, yb, w->w, span_bytes(w->n, w->k, w->k)) ||
       overlap(y, yb, w->bias, static_cast<size_t>(w->n) * 2) ||
-      (residual && (residual != y || ld_residual != ldy) &&
-       overlap(y, yb, residual, span_bytes(M, w->n, ld_residual))))
+      (residual && (residual != y || ld_residual != ldy) && overlap(yr, {residual, M, w->n, ld_residual})))
     return fail(QI_ERR_INVALID_ARG, "y overlaps an input (only residual == y with the same ld is allowed)");
   if (M == 0) return QI_OK;
   qi::LinearActParams p;
@@ -324,7 +341,7 @@ int qi_gated_ffn_forward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x, 
       overlap(workspace, workspace_bytes, w->down, wb) || overlap(workspace, workspace_bytes, w->gate, wb) ||
       overlap(workspace, workspace_bytes, w->up, wb) ||
       (residual && (residual != y || ld_residual != ldy) &&
-       overlap(y, yb, residual, span_bytes(M, H, ld_residual))))
+       overlap({y, M, H, ldy}, Rows{residual, M, H, ld_residual})))
     return fail(QI_ERR_INVALID_ARG, "gated ffn: an output overlaps an input, the workspace or the other output");
   qi::GateUpParams g;
   g.x = x;
@@ -381,6 +398,7 @@ int qi_gated_ffn_backward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x,
     return r;
   const size_t wb = static_cast<size_t>(H) * F * 2, xb = span_bytes(M, H, ldx), yb = span_bytes(M, H, ld_dy),
                gb = static_cast<size_t>(M) * 2 * F * 4;
+  const Rows xr{x, M, H, ldx}, yr{dy, M, H, ld_dy}, dr{dx, M, H, ld_dx};
   struct Range {
     const void* p;
     size_t n;
@@ -389,13 +407,16 @@ int qi_gated_ffn_backward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x,
                          {workspace, workspace_bytes}};
   const Range ins[6] = {{x, xb}, {dy, yb}, {gate_up, gb}, {w->gate, wb}, {w->up, wb}, {w->down, wb}};
   for (int i = 0; i < 5; ++i) {
-    for (const Range& in : ins)
-      if (overlap(outs[i].p, outs[i].n, in.p, in.n))
+    for (int j = 0; j < 6; ++j)
+      if (i == 0 && j < 2 ? overlap(dr, j == 0 ? xr : yr) : overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n))
         return fail(QI_ERR_INVALID_ARG, "gated ffn backward: an output or the workspace overlaps an input");
     for (int j = 0; j < i; ++j)
       if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
         return fail(QI_ERR_INVALID_ARG, "gated ffn backward: outputs or the workspace overlap");
   }
+  if (M > 0 && !dx && !dgate && !dup && !ddown) return QI_OK;
+  Carve c{nullptr, 0, 0};
+  if (M > 0 && (r = take_workspace(workspace, workspace_bytes, gated_bytes(*w, M, true), &c))) return r;
   DeviceScope dev(ctx);
   if (!dev.ok) return cuda_fail("cudaSetDevice");
   if (M == 0) {   // a sum over no rows
@@ -403,9 +424,6 @@ int qi_gated_ffn_backward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x,
       if (p && cudaMemsetAsync(p, 0, wb, S(stream)) != cudaSuccess) return cuda_fail("zero gradient");
     return QI_OK;
   }
-  if (!dx && !dgate && !dup && !ddown) return QI_OK;
-  Carve c{nullptr, 0, 0};
-  if ((r = take_workspace(workspace, workspace_bytes, gated_bytes(*w, M, true), &c))) return r;
   const GatedBufs b = carve_gated(c, M, F, true);
   qi::GatedBackwardParams p;
   p.x = x;

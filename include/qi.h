@@ -371,7 +371,9 @@ int qi_attn_split_plan(int Sk, int heads, const qi_groups* groups, int num_sms,
  * graph.  Two calls may run at the same time on different streams, from
  * different contexts if from different host threads, as long as their
  * outputs and workspaces are different memory.  An
- * output must not overlap an input or the workspace unless the call says so.
+ * output must not overlap an input or the workspace unless the call says so
+ * (column ranges of the same rows, such as the parts of one fused q | k | v | o
+ * block, do not overlap).
  * Rows, columns, K and the queries or keys of a sequence: at most 2^30 (mlp: 2^29). */
 
 /* Causal attention over packed sequences with grouped heads:

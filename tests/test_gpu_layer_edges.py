@@ -138,3 +138,52 @@ def test_first_calls_from_several_threads(ctx):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr
+
+
+@pytest.mark.parametrize("T", [1, 70, 700])
+def test_outputs_between_the_columns_of_their_inputs(ctx, T):
+    """q | k | v | o, x | y | residual and x | dx | dy as column ranges of one block
+    of rows: the bits of separate buffers, and the other columns as they were."""
+    heads, kvh, H, F = 8, 2, 256, 520
+    W, KW = heads * 128, kvh * 128
+    block = rand(T, 2 * W + 2 * KW + 64, seed=3)
+    before = block.clone()
+    q, k, v, o = (block[:, a:b] for a, b in ((0, W), (W, W + KW), (W + KW, W + 2 * KW), (W + 2 * KW, 2 * W + 2 * KW)))
+    spans = torch.tensor([[0, T, 0, T]], dtype=torch.int32)
+    want = qi.qi_attn_causal_packed(ctx, *(t.contiguous() for t in (q, k, v)), spans, heads, kvh)
+    qi.qi_attn_causal_packed(ctx, q, k, v, spans, heads, kvh, o=o)
+    ctx.check()
+    assert same_bits(o, want)
+    o.copy_(before[:, W + 2 * KW:2 * W + 2 * KW])
+    assert same_bits(block, before)
+
+    for n, at in ((136, 2 * H), (131, 2 * H - 1)):     # rows that are 16-byte aligned, and not
+        block = rand(T, 3 * H, seed=4)
+        before = block.clone()
+        a, y, res = block[:, :H], block[:, H:H + n], block[:, at:at + n]
+        w = qi.bf16_struct(rand(n, H, seed=5, scale=0.05), rand(n, seed=6))
+        want = qi.qi_linear_act(ctx, a.contiguous(), w, qi.QI_ACT_SILU, residual=res.contiguous())
+        qi.qi_linear_act(ctx, a, w, qi.QI_ACT_SILU, residual=res, y=y)
+        ctx.check()
+        # (other rows may take another kernel, and another order of the sums: two roundings of sums that
+        # differ by 2 (k / 16 + 2) 2^-23 sum |a w| < 2^-14 at most)
+        assert ((y.double() - want.double()).abs() <= 2 * U * want.double().abs() + 2.0 ** -14).all()
+        y.copy_(before[:, H:H + n])
+        assert same_bits(block, before)
+
+    ffn = qi.gated_ffn_struct(rand(F, H, seed=7, scale=H ** -0.5), rand(F, H, seed=8, scale=H ** -0.5),
+                              rand(H, F, seed=9, scale=F ** -0.5))
+    block = rand(T, 3 * H, seed=10)
+    before = block.clone()
+    x, dx, dy = block[:, :H], block[:, H:2 * H], block[:, 2 * H:]
+    want, saved = qi.qi_gated_ffn_forward(ctx, ffn, x, save=True)
+    full = qi.qi_gated_ffn_backward(ctx, ffn, x.contiguous(), dy.contiguous(), saved)
+    got = qi.qi_gated_ffn_backward(ctx, ffn, x, dy, saved, dx=dx)
+    ctx.check()
+    assert all(same_bits(s, t) for s, t in zip(got, full))
+    dx.copy_(before[:, H:2 * H])
+    assert same_bits(block, before)
+    qi.qi_gated_ffn_forward(ctx, ffn, x, residual=dy, y=dx)
+    plain = qi.qi_gated_ffn_forward(ctx, ffn, x.contiguous(), residual=dy.contiguous())
+    ctx.check()
+    assert same_bits(dx, plain) and same_bits(dy, before[:, 2 * H:]) and same_bits(x, before[:, :H])

@@ -124,6 +124,41 @@ def test_product_sizes_past_the_index_range(L, dummy):
                                                None), SHAPE, "2^")
 
 
+def test_columns_of_one_block_are_no_overlap(L, dummy):
+    """Columns of one block of rows share no byte although their address ranges
+    interleave: the calls get past the check (to the next one, of the workspace)."""
+    ld = 512 + 256 + 256 + 512
+    kw = dict(q=16 * P, k=16 * P + 1024, v=16 * P + 1536, q_rows=8192, k_rows=8192, ldq=ld, ldk=ld, ldv=ld, ldo=ld)
+    t = [(0, 1, 0, 8192)]
+    assert refused(attn(L, dummy, t, o=16 * P + 2048, **kw), WS, "workspace")
+    # one row of queries, whose own distance says nothing
+    assert refused(attn(L, dummy, t, o=16 * P + 2048, **dict(kw, q_rows=1, ldq=512, ldo=512)), WS, "workspace")
+    w = qi.qi_gated_ffn()
+    w.gate, w.up, w.down, w.hidden, w.mlp, w.act = P, 2 * P, 3 * P, 64, 128, qi.QI_ACT_SILU
+    got = L.qi_gated_ffn_backward(C.addressof(dummy), C.byref(w), 4 * P, 4, 192, 4 * P + 256, 192, 7 * P, 4 * P + 128,
+                                  192, None, None, None, None, 0, None)
+    assert refused(got, WS, "workspace")
+
+
+def test_columns_that_share_bytes_are_refused(L, dummy):
+    """One column too many, behind the block's end and around it, and another row distance."""
+    t = [(0, 4, 0, 4)]
+    ld = 512 + 256 + 256 + 512
+    kw = dict(q=16 * P, k=16 * P + 1024, v=16 * P + 1536, k_rows=16, ldq=ld, ldk=ld, ldv=ld, ldo=ld)
+    for off in (2032, 2064, 2048 + 2 * ld + 16, 2048 - 16 - 2 * ld):
+        assert refused(attn(L, dummy, t, o=16 * P + off, **kw), INV, "o overlaps")
+    assert refused(attn(L, dummy, t, o=16 * P + 2048, **dict(kw, ldo=ld + 8)), INV, "o overlaps")
+    w = qi.qi_gated_ffn()
+    w.gate, w.up, w.down, w.hidden, w.mlp, w.act = P, 2 * P, 3 * P, 64, 128, qi.QI_ACT_SILU
+    for off in (112, 144, 256):
+        got = L.qi_gated_ffn_backward(C.addressof(dummy), C.byref(w), 4 * P, 4, 192, 4 * P + 256, 192, 7 * P,
+                                      4 * P + off, 192, None, None, None, None, 0, None)
+        assert refused(got, INV, "overlaps an input")
+    for kw in (dict(lda=104, y=P + 126, ldy=104), dict(lda=104, y=P + 130, ldy=104), dict(lda=104, y=P + 128, ldy=105),
+               dict(lda=152, y=P + 128, ldy=152, res=P + 206, ldr=152)):
+        assert refused(linear(L, dummy, a=P, **kw), INV, "y overlaps")
+
+
 # ------------------------------------------------------------------ binding
 
 def zeros(*shape, dtype=torch.bfloat16, device="cpu"):
