@@ -187,3 +187,161 @@ def test_outputs_between_the_columns_of_their_inputs(ctx, T):
     plain = qi.qi_gated_ffn_forward(ctx, ffn, x.contiguous(), residual=dy.contiguous())
     ctx.check()
     assert same_bits(dx, plain) and same_bits(dy, before[:, 2 * H:]) and same_bits(x, before[:, :H])
+
+
+# ------------------------------------------------------------------ every key of a split range
+
+def peaked(k, kvh, j, r, a=60.0):
+    """Queries [n, heads * 128] that put about half of their weight each on the keys
+    j[i, h] and r[i, h] of their key/value head: q scale = a (k_j / |k_j|^2 + k_r / |k_r|^2),
+    so both score about a and the rest at most half of it (128 columns: |k_i k_j| is
+    a tenth of |k|^2, five times that at most)."""
+    n, heads = j.shape
+    K = k.double().view(-1, kvh, 128)
+    head = (torch.arange(heads, device="cuda") // (heads // kvh)).expand(n, heads)
+    q = sum(K[x, head] / K[x, head].pow(2).sum(-1, keepdim=True) for x in (j, r))
+    return (q * a * 128 ** 0.5).reshape(n, heads * 128).to(BF)
+
+
+def check_peaked(q, k, v, spans, kvh, got, causal=True):
+    """Against the formula in 64 bits; a key lost or counted twice would move the
+    output by a third of a value at least, of which the tolerance (the weights' and
+    the output's rounding to bf16, 2^-12 for the rest) is a hundredth."""
+    heads = q.shape[1] // 128
+    for q0, ql, k0, kl in spans:
+        see = torch.arange(kl, device="cuda")[None] <= kl - ql + torch.arange(ql, device="cuda")[:, None]
+        for h in range(heads):
+            c, e = slice(h * 128, h * 128 + 128), h // (heads // kvh)
+            kv = slice(e * 128, e * 128 + 128)
+            s = q[q0:q0 + ql, c].double() @ k[k0:k0 + kl, kv].double().T * 128 ** -0.5
+            if causal:
+                s = s.masked_fill(~see, -np.inf)
+            p, V = torch.softmax(s, -1), v[k0:k0 + kl, kv].double()
+            o, mag = p @ V, p @ V.abs()
+            assert ((got[q0:q0 + ql, c].double() - o).abs() <= U * o.abs() + (U * (1 + U) + 2.0 ** -12) * mag).all()
+
+
+def test_token_every_key_of_a_split_range(ctx):
+    """One token on 8191 keys, split over ranges: every key in turn carries half of
+    the weight of one head, so one that is left out or taken twice shows."""
+    heads, kvh, n = 8, 2, 8191
+    k, v = rand(n, kvh * 128, seed=1), rand(n, kvh * 128, seed=2)
+    calls = -(-n // 4)                         # 4 heads on each key/value head
+    j = (torch.arange(calls * 4, device="cuda").view(calls, 1, 4) % n).expand(calls, 2, 4).reshape(calls, heads)
+    r = (j + 3001 + 7 * torch.arange(calls, device="cuda")[:, None]) % n
+    q = peaked(k, kvh, j, r)
+    one = torch.tensor([[0, 1, 0, n]], dtype=torch.int32)
+    assert qi.qi_attn_causal_packed_workspace_bytes(ctx, one, heads, kvh) > 0
+    o = torch.empty_like(q)
+    for i in range(calls):
+        qi.qi_attn_causal_packed(ctx, q[i:i + 1], k, v, one, heads, kvh, o=o[i:i + 1])
+    ctx.check()
+    check_peaked(q, k, v, [(0, calls, 0, n)], kvh, o, causal=False)   # (a call each: all see all the keys)
+
+
+def test_tokens_every_key_of_longer_ranges(ctx):
+    """256 tokens that share 8191 keys (their ranges are longer than a single token's)."""
+    heads, kvh, n, T = 8, 2, 8191, qi.QI_MAX_SEQS
+    k, v = rand(n, kvh * 128, seed=1), rand(n, kvh * 128, seed=2)
+    spans = [(i, 1, 0, n) for i in range(T)]
+    for first in range(0, n, T * 4):
+        j = ((first + torch.arange(T * 4, device="cuda")) % n).view(T, 1, 4).expand(T, 2, 4).reshape(T, heads)
+        r = (j + 2999 + 13 * torch.arange(T, device="cuda")[:, None]) % n
+        q = peaked(k, kvh, j, r)
+        got = qi.qi_attn_causal_packed(ctx, q, k, v, torch.tensor(spans, dtype=torch.int32), heads, kvh)
+        ctx.check()
+        check_peaked(q, k, v, spans, kvh, got)
+
+
+@pytest.mark.parametrize("ql,kl", [(300, 5000), (40, 3000), (2, 6001)])
+def test_prompt_every_key_of_a_split_range(ctx, ql, kl):
+    """Queries behind cached keys on tiles (and two rows of tokens) whose keys are
+    split: every key carries weight somewhere, and at the diagonal the last key
+    that a query sees and the first it does not."""
+    heads, kvh = 8, 2
+    k, v = rand(kl, kvh * 128, seed=1), rand(kl, kvh * 128, seed=2)
+    table = torch.tensor([[0, ql, 0, kl]], dtype=torch.int32)
+    assert qi.qi_attn_causal_packed_workspace_bytes(ctx, table, heads, kvh) > 0
+    i = torch.arange(ql, device="cuda")
+    last = (kl - ql + i)[:, None, None]                    # the last key that query i sees
+    step = torch.arange(ql * 4, device="cuda").view(ql, 1, 4)
+    picks = [(first + step) % (kl - ql + 1) for first in range(0, kl - ql + 1, ql * 4)]   # seen by every query
+    picks += [(last - torch.arange(4, device="cuda") - 4 * a).clamp(min=0) for a in range(2)]
+    picks.append((last + 1 + torch.arange(4, device="cuda")).clamp(max=kl - 1))            # past the diagonal
+    for n, j in enumerate(picks):
+        j = j.expand(ql, 2, 4).reshape(ql, heads)
+        r = (j + 1009 + 17 * n) % (kl - ql + 1)
+        q = peaked(k, kvh, j, r)
+        got = qi.qi_attn_causal_packed(ctx, q, k, v, table, heads, kvh)
+        ctx.check()
+        check_peaked(q, k, v, [(0, ql, 0, kl)], kvh, got)
+
+
+# ------------------------------------------------------------------ buffers of more than 2^31 values
+
+@pytest.mark.parametrize("n,shift", [(40, 0), (41, 1)])
+def test_linear_rows_past_2_to_31_values(ctx, n, shift):
+    """Inputs, residual and outputs whose offsets pass 2^31 values and 2^32 bytes:
+    aligned rows (TMA) and rows at odd addresses (single values)."""
+    M, ld, k = 530000, 4096, 64
+    block = torch.zeros(M, ld, dtype=BF, device="cuda")
+    a, y, res = block[:, :k], block[:, 128 + shift:128 + shift + n], block[:, 256 + shift:256 + shift + n]
+    a.copy_(rand(M, k, seed=1))
+    res.copy_(rand(M, n, seed=2))
+    w, b = rand(n, k, seed=3, scale=0.1), rand(n, seed=4)
+    qi.qi_linear_act(ctx, a, qi.bf16_struct(w, b), qi.QI_ACT_SILU, residual=res, y=y)
+    ctx.check()
+    at = torch.cat([torch.arange(0, M, 997), torch.arange(2 ** 31 // ld - 300, 2 ** 31 // ld + 300),
+                    torch.arange(2 ** 30 // ld - 300, 2 ** 30 // ld + 300), torch.arange(M - 300, M)]).cuda()
+    A = a[at].double()
+    ref = A @ w.double().T + b.double()
+    ref = ref * torch.sigmoid(ref)
+    tol = acc_tol(A, w.double()) + 2.0 ** -16 * ref.abs()
+    ref = ref + res[at].double()
+    assert ((y[at].double() - ref).abs() <= tol + U * ref.abs()).all()
+    assert not block[:, 128 + shift + n:256].any() and not block[:, 64:128 + shift].any()
+
+
+def test_gated_ffn_buffers_past_2_to_31_values(ctx):
+    """Hidden values, saved gate | up and the backward scratch past 2^31 values: rows on
+    both sides of the border, and gradients of the weights that come from them alone."""
+    M, H, F = 140000, 64, 16384
+    border = 2 ** 31 // F                      # row of h that begins at value 2^31
+    x = rand(M, H, seed=1)
+    wg, wu, wd = rand(F, H, seed=2, scale=H ** -0.5), rand(F, H, seed=3, scale=H ** -0.5), rand(H, F, seed=4,
+                                                                                           scale=F ** -0.5)
+    ffn = qi.gated_ffn_struct(wg, wu, wd)
+    y, saved = qi.qi_gated_ffn_forward(ctx, ffn, x, save=True)
+    at = torch.cat([torch.arange(0, 300), torch.arange(border // 2 - 150, border // 2 + 150),
+                    torch.arange(border - 150, border + 150), torch.arange(M - 300, M)]).cuda()
+    dy = torch.zeros(M, H, dtype=BF, device="cuda")
+    dy[at] = rand(len(at), H, seed=5)
+    got = qi.qi_gated_ffn_backward(ctx, ffn, x, dy, saved)
+    ctx.check()
+    X, Y, G, W, D = x[at].double(), dy[at].double(), wg.double(), wu.double(), wd.double()
+    g, u = X @ G.T, X @ W.T
+    tg, tu = acc_tol(X, G), acc_tol(X, W)
+    assert ((saved[at, :F].double() - g).abs() <= tg).all() and ((saved[at, F:].double() - u).abs() <= tu).all()
+    g, u = saved[at, :F].double(), saved[at, F:].double()
+    s = torch.sigmoid(g)
+    act, slope = g * s, s * (1 + g * (1 - s))
+    h, th = act * u, (U + 2.0 ** -16) * (act * u).abs()
+    ref = h @ D.T
+    tol = th @ D.abs().T + acc_tol(h, D) * (1 + U)
+    assert ((y[at].double() - ref).abs() <= tol + U * (ref.abs() + tol)).all()
+    # one rounding of dg, du and h to bf16, 2^-16 for the activations (the slope: 2^-17 of its terms, below
+    # 1.2 (1 + |g|)), the fp32 sums, one rounding of each gradient
+    eps = U * (1 + U) + 2.0 ** -16
+    dh, tdh = Y @ D, acc_tol(Y, D.T)
+    dg, tdg = dh * u * slope, (eps * slope.abs() + 2.0 ** -17 * 1.2 * (1 + g.abs())) * (dh * u).abs() + tdh * (u * slope).abs()
+    du, tdu = dh * act, eps * (dh * act).abs() + tdh * act.abs()
+    h, th = act * u, eps * (act * u).abs()
+    rows = 2.0 ** -23 * (M / 16 + 2) * 1.13    # sums over all M rows, of which the others are 0
+    refs = [(dg @ G + du @ W, tdg @ G.abs() + tdu @ W.abs() + acc_tol(dg, G.T) + acc_tol(du, W.T)),
+            (dg.T @ X, tdg.T @ X.abs() + rows * (dg.abs().T @ X.abs())),
+            (du.T @ X, tdu.T @ X.abs() + rows * (du.abs().T @ X.abs())),
+            (Y.T @ h, Y.abs().T @ th + rows * (Y.abs().T @ h.abs()))]
+    for i, (t, (ref, tol)) in enumerate(zip(got, refs)):
+        t = (t[at] if i == 0 else t).double()
+        assert ((t - ref).abs() <= 1.01 * tol + U * (ref.abs() + tol) + 1e-30).all()
+    assert not got[0][300:border // 2 - 150].any()      # dx of rows without a gradient
