@@ -310,9 +310,10 @@ __device__ __forceinline__ void mm_fetch(const MmMaps& maps, MmStage& s, int row
 // nobody waits for could reach the even CTA after its exit.  A thread holds one row, so its own accesses would be
 // 16 bytes in each of 32 rows, 32 passes of the load/store unit each; instead a
 // warp's 32 x 32 chunk goes through shared memory and TMA brings the inputs and
-// takes the outputs (TMA keeps to the rows and columns that exist).  TMA needs
-// rows that are 16-byte aligned; others (p.vec == 0) are read and written by
-// the warp, one value per lane and 32 of a row at a time.
+// takes the outputs (TMA keeps to the rows that exist, and to the columns in
+// whole groups of 16 bytes).  TMA needs rows that are 16-byte aligned; others
+// (p.vec == 0) are read, and they and a chunk that N cuts inside such a group
+// are written, by the warp, one value per lane and 32 of a row at a time.
 // Swizzles: 16-byte group q of row r of a bf16 chunk lies at q ^ (r / 2 mod 4),
 // of an fp32 chunk at q ^ (r mod 8).
 template <int EPI>
@@ -414,14 +415,16 @@ __device__ __forceinline__ bool mm_epilogue(const MmMaps& maps, const MmParams& 
         mm_math8<EPI>(p, v, u, col0 + q * 8, N - col0 - q * 8, x, xg, xu, o0, o1, o2);
         put(at, q, o0);
       }
-      if (vec) {
+      if (vec && (N % 8 == 0 || col0 + 32 <= N)) {
         send(&maps.y[pr], at, col0, 0);
       } else {
+        if (lane == 0) bulk_commit_group();   // (one group per chunk, if an empty one, for the waits that count them)
         __syncwarp();
         uint16_t* dst = p.y[pr] + static_cast<size_t>(row0) * p.ldy[pr] + col0 + lane;
         if (col_in)
 #pragma unroll 8
           for (int i = 0; i < rows; ++i) dst[static_cast<size_t>(i) * p.ldy[pr]] = *value(i);
+        fence_proxy_async_smem();   // read before TMA writes the chunk again
         __syncwarp();
       }
       ++s.turn;

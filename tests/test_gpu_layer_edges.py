@@ -345,3 +345,22 @@ def test_gated_ffn_buffers_past_2_to_31_values(ctx):
         t = (t[at] if i == 0 else t).double()
         assert ((t - ref).abs() <= 1.01 * tol + U * (ref.abs() + tol) + 1e-30).all()
     assert not got[0][300:border // 2 - 150].any()      # dx of rows without a gradient
+
+
+@pytest.mark.parametrize("M", [1, 12, 60, 300, 700, 1300])
+@pytest.mark.parametrize("n", [1, 3, 131, 2301])
+def test_linear_odd_outputs_in_aligned_rows(ctx, M, n):
+    """An odd number of columns in rows that are 16-byte aligned (y and residual parts
+    of padded buffers): nothing behind the last column is written."""
+    k, pad = 136, -(-n // 8) * 8 + 8
+    a, w, b = rand(M, k), rand(n, k, seed=1, scale=0.1), rand(n, seed=2)
+    res, out = rand(M, pad, seed=3), rand(M + 1, pad, seed=4)
+    before = out.clone()
+    qi.qi_linear_act(ctx, a, qi.bf16_struct(w, b), qi.QI_ACT_SILU, residual=res[:, :n], y=out[:M, :n])
+    ctx.check()
+    ref = a.double() @ w.double().T + b.double()
+    ref = ref * torch.sigmoid(ref)
+    tol = acc_tol(a.double(), w.double()) + 2.0 ** -16 * ref.abs()
+    ref = ref + res[:, :n].double()
+    assert ((out[:M, :n].double() - ref).abs() <= tol + U * ref.abs()).all()
+    assert same_bits(out[:M, n:], before[:M, n:]) and same_bits(out[M:], before[M:])
