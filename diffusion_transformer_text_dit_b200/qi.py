@@ -373,7 +373,7 @@ def bf16_struct(w, bias=None) -> qi_linear_bf16:
     s = qi_linear_bf16()
     s.w, s.bias = ptr(w), ptr(bias)
     s.n, s.k = w.shape
-    s._keep = (w, bias)
+    s._keep, s._device = (w, bias), w.get_device()
     return s
 
 
@@ -536,10 +536,9 @@ def _rows(ctx: Context, t: Optional[torch.Tensor], name: str, cols: int):
 
 def _weights_here(ctx: Context, w):
     """Checks that the tensors behind a weight struct are on the context's device
-    (a struct's maker has checked that they are all on one)."""
-    keep = getattr(w, "_keep", None)
-    if keep is not None and keep[0].get_device() != ctx.device:
-        raise ValueError(f"the weights must be on cuda:{ctx.device}, not {keep[0].device}")
+    (the struct's maker has checked that they are all on one and kept its index)."""
+    if getattr(w, "_device", ctx.device) != ctx.device:
+        raise ValueError(f"the weights must be on cuda:{ctx.device}, not {w._keep[0].device}")
 
 
 def _whole(t: Optional[torch.Tensor], name: str, shape, like: torch.Tensor, dtype=torch.bfloat16):
@@ -658,7 +657,7 @@ def gated_ffn_struct(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
         raise ValueError("gated ffn weights must be on one device")
     s = qi_gated_ffn()
     s.gate, s.up, s.down, s.hidden, s.mlp, s.act = ptr(gate), ptr(up), ptr(down), H, F, act
-    s._keep = (gate, up, down)
+    s._keep, s._device = (gate, up, down), gate.get_device()
     return s
 
 

@@ -455,7 +455,8 @@ int qi_gated_ffn_forward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x, 
  * are rounded to bf16 once as operands of the products that follow; g, u and
  * every sum are fp32 and every gradient is rounded to bf16 once.  Each of dx [M, hidden],
  * dgate, dup [mlp, hidden], ddown [hidden, mlp] may be NULL (not wanted); the
- * others are overwritten, in the same bits on every call (no atomics).  With
+ * others are overwritten, in the same bits every time the same call is made (no
+ * atomics; which gradients are wanted may change the order of a sum).  With
  * M = 0 the weights' gradients are set to 0.  A row of dy, x or gate_up whose
  * values are not finite makes the weights' gradients not finite. */
 int qi_gated_ffn_backward(qi_ctx* ctx, const qi_gated_ffn* w, const uint16_t* x, int M, int ldx,

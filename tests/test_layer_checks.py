@@ -198,6 +198,7 @@ def test_weights_on_another_device_than_the_context():
     lin, ffn = qi.qi_linear_bf16(), qi.qi_gated_ffn()
     lin.n, lin.k, ffn.hidden, ffn.mlp = 4, 8, 8, 16
     lin._keep, ffn._keep = (zeros(4, 8), None), (zeros(16, 8), zeros(16, 8), zeros(8, 16))
+    lin._device = ffn._device = -1        # (a host tensor's)
     x, gu = zeros(2, 8), zeros(2, 32, dtype=torch.float32)
     for call in (lambda: qi.qi_linear_act(Ctx, x, lin, stream=Stream),
                  lambda: qi.qi_gated_ffn_forward(Ctx, ffn, x, stream=Stream),
