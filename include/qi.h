@@ -364,11 +364,15 @@ int qi_attn_split_plan(int Sk, int heads, const qi_groups* groups, int num_sms,
  * text input of a step).  With rows x of several packed prompts:
  *   qkv = qi_linear_act(x);  o = qi_attn_causal_packed(q, k, v);
  *   x   = qi_linear_act(o) + x;  x = qi_gated_ffn_forward(x) + x
- * (norms and rotary embedding in between).  The pages describe no such call.
+ * Norms and rotary embedding in between are the caller's: qi_qk_norm_rope takes
+ * equal numbers of query and key heads in one [T, 3 hidden] block, so it does not
+ * serve grouped heads, and there is no call for a layer's own norm.  The block has
+ * a backward call; the Linear and the attention have none (nor does the attention
+ * return its softmax statistics).  The pages describe no such call.
  * These calls work whichever device is current (the context's is made current
  * for the call and the former one restored), use no state of the context other
- * than its status word and launch counters, and may be captured into a CUDA
- * graph.  Two calls may run at the same time on different streams, from
+ * than its status word and launch counters (with profiling on, its events), and
+ * may be captured into a CUDA graph.  Two calls may run at the same time on different streams, from
  * different contexts if from different host threads, as long as their
  * outputs and workspaces are different memory.  An
  * output must not overlap an input or the workspace unless the call says so
